@@ -3,7 +3,8 @@
  *
  * These launch, one at a time, the same sm_100a kernels that wan_dit_forward()
  * strings together, so each step of the Wan DiT forward can be checked on its
- * own.  Citations name the page and section whose computation the kernel
+ * own, and the attention operators over parts of the sequence (selected key
+ * blocks, a paged cache), which the forward does not call.  Citations name the page and section whose computation the kernel
  * performs (see wandit.h for the page list).  Conventions are those of
  * wandit.h: plain device pointers, `stream` is a cudaStream_t as void*, calls
  * are asynchronous, nothing is retained after the call, shape errors are
@@ -109,6 +110,118 @@ WANDIT_API wan_status wan_op_attention_qnorm(const void* q, int64_t ldq, const v
                             const void* v, int64_t ldv, void* o, int64_t ldo,
                             int B, int heads, int Lq, int Lk,
                             const float* q_ssq, int64_t ssq_ld, int ngroups, float eps, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention over parts of the sequence.  The tokens of q and of k / v lie on
+ * grids (frames, rows, columns; token (f * H + i) * W + j, as patchify orders
+ * them; a plain sequence of L tokens is the grid 1 x 1 x L).  Boxes of qb_F x
+ * qb_H x qb_W query tokens and kb_F x kb_H x kb_W key tokens cut the grids into
+ * blocks, numbered like the tokens; the blocks at a grid's far edges hold the
+ * tokens that are left.  Limits: every extent >= 1; at most 128 tokens per query
+ * block; 16, 32, 64 or 128 per key block (the box's volume).                 */
+typedef struct {
+    int q_F, q_H, q_W;      /* query token grid                                */
+    int k_F, k_H, k_W;      /* key token grid                                  */
+    int qb_F, qb_H, qb_W;   /* query block                                     */
+    int kb_F, kb_H, kb_W;   /* key block                                       */
+} wan_block_grid;
+
+/* Key blocks for block-sparse attention.  Per sample and head, query block i
+ * scores key block j by the dot product of the mean of its queries and the mean
+ * of the block's keys (held in 64 bits: the order of additions does not decide
+ * between close scores) and keeps the topk best: equal scores go to the lower
+ * block, a NaN ranks with -inf.  mask: uint8 [query blocks, key blocks] shared
+ * by samples and heads, or NULL; 0 forbids a block, 1 leaves it to its score,
+ * any other value takes it ahead of all scores.
+ *   blocks  int32 [B, heads, query blocks, topk]: the blocks kept, ascending,
+ *           then -1 where fewer than topk are allowed
+ *   counts  int32 [B, heads, query blocks]: how many are kept
+ * q, k: rows (b, l) at q + (b * L + l) * ldq, head h in columns [128 h, 128 h +
+ * 128), bf16.  workspace: device memory of at least
+ * wan_op_block_select_workspace() bytes (16-byte aligned); it must not be used
+ * by anything else until the call's kernels have run: calls on different
+ * streams, and graphs that may be replayed at the same time, need their own.
+ * Errors before any launch: WAN_EINVAL for a null pointer, WAN_ESHAPE for sizes
+ * outside the limits above, topk outside [1, key blocks], more than 28800 key
+ * blocks, B * heads > 65535, a leading dimension below 128 * heads or not a
+ * multiple of 8, pointers of q, k or workspace that are not 16-byte aligned or
+ * a workspace that is too small.  B = 0 launches nothing.                    */
+WANDIT_API wan_status wan_op_block_select(const void* q, int64_t ldq, const void* k, int64_t ldk, int B, int heads,
+                                          const wan_block_grid* g, const uint8_t* mask, int topk, int32_t* blocks,
+                                          int32_t* counts, void* workspace, int64_t workspace_bytes, void* stream);
+/* Bytes of its workspace; -1 for sizes it refuses. */
+WANDIT_API int64_t wan_op_block_select_workspace(int B, int heads, const wan_block_grid* g);
+
+/* Block-sparse attention: O = softmax(Q K^T / sqrt(128)) V, each query over the
+ * tokens of the key blocks that are listed for its query block and head (blocks
+ * and counts as wan_op_block_select writes them; the first counts[..] entries of
+ * a list are read, a count is held to [0, topk]).  An entry that is no block of
+ * the key grid is skipped; one listed twice counts twice.  A query whose list
+ * holds nothing gets a zero row, and -inf in lse.
+ *   lse   f32 [B, heads, query tokens], log of the softmax denominator with the
+ *         row maximum in it (natural logarithm), or NULL
+ *   workspace  as above, wan_op_attention_blocks_workspace() bytes; may be NULL
+ *         where that is 0 (it is, unless the query tiles are too few to fill the
+ *         GPU: then each list is split and the parts are joined)
+ * Layouts as wan_op_attention; errors as wan_op_block_select (topk >= 1).     */
+WANDIT_API wan_status wan_op_attention_blocks(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v,
+                                              int64_t ldv, void* o, int64_t ldo, int B, int heads,
+                                              const wan_block_grid* g, const int32_t* blocks, const int32_t* counts,
+                                              int topk, float* lse, void* workspace, int64_t workspace_bytes,
+                                              void* stream);
+WANDIT_API int64_t wan_op_attention_blocks_workspace(int B, int heads, const wan_block_grid* g, int topk);
+
+/* Keys and values of several sequences in pages: token r of page p at
+ * k + p * page_stride + r * token_stride (elements, both multiples of 8; head h
+ * in columns [128 h, 128 h + 128)), and at the same place of v.  Place s of
+ * sequence b lies in page table[b * table_ld + s / page_size], at s % page_size.
+ * Table entries outside [0, num_pages) hold nothing: they are not written, and
+ * attention skips their places.  page_size 16, 32, 64 or 128.                */
+typedef struct {
+    void* k;
+    void* v;
+    int64_t page_stride, token_stride;
+    int num_pages, page_size;
+    const int32_t* table;   /* [B, max_pages]                                  */
+    int64_t table_ld;
+    int max_pages;          /* pages per sequence                              */
+} wan_kv_cache;
+
+/* Append T new tokens per sequence to a cache, rotated on the way: token t <
+ * count[b] (count NULL: T) of sequence b goes to place s = start[b] + t.  Its key
+ * row (b * T + t) is multiplied by its RMSNorm factor across heads and by
+ * k_gain[128 * heads] (k_gain NULL: neither), turned by the 3-axis RoPE of grid
+ * position (s / (H W), s / W % H, s % W) when rope != 0 (frames have no limit;
+ * split and pairs as wan_op_rmsnorm_rope), rounded once and stored; the value
+ * row is copied.  With q != NULL the query rows get q_gain's norm and the same
+ * rotation into q_out (may be q itself).  Rows t >= count[b], places past the
+ * table (start[b] < 0 too) and pages that are not there are left as they were
+ * (q_out is written for every t < count[b] with start[b] >= 0).  Two sequences
+ * that share a page must not write the same place.
+ * Errors before any launch: WAN_EINVAL for a null pointer, WAN_ESHAPE for B, T <
+ * 0, heads <= 0, a RoPE split that is not even with sum 128, H, W <= 0, theta <=
+ * 0, strides or pointers (k, v, q, q_out, the cache, gains) that are not
+ * 16-byte aligned, a leading dimension or token stride below 128 * heads, a
+ * page stride that lets pages overlap, or a cache outside the limits above.   */
+WANDIT_API wan_status wan_op_kv_append(const void* k, int64_t ldk, const void* v, int64_t ldv, int B, int T, int heads,
+                                       const int32_t* start, const int32_t* count, const float* k_gain, float eps,
+                                       int rope, int H, int W, int rope_t, int rope_h, int rope_w, float theta,
+                                       const void* q, int64_t ldq, const float* q_gain, void* q_out, int64_t ldqo,
+                                       const wan_kv_cache* cache, void* stream);
+
+/* Attention of T >= 1 new tokens per sequence over its cache: O = softmax(Q K^T /
+ * sqrt(128)) V over places [0, lens[b]) (lens[b] is held to [0, max_pages *
+ * page_size]), without a mask among the new tokens: tokens of one chunk see each
+ * other, as in a bidirectional forward, once they are appended.  Row (b, t) of q
+ * / o at q + (b * T + t) * ldq.  lens[b] = 0 gives zero rows and -inf in lse
+ * (f32 [B, heads, T], or NULL).  Memory of a page past the sequence's end is not
+ * read into the result, whatever it holds.  Long caches are split and joined when
+ * the query tiles are few: workspace as above,
+ * wan_op_attention_paged_workspace() bytes.                                  */
+WANDIT_API wan_status wan_op_attention_paged(const void* q, int64_t ldq, const wan_kv_cache* cache,
+                                             const int32_t* lens, void* o, int64_t ldo, int B, int heads, int T,
+                                             float* lse, void* workspace, int64_t workspace_bytes, void* stream);
+WANDIT_API int64_t wan_op_attention_paged_workspace(int B, int heads, int T, const wan_kv_cache* cache);
 
 /* In-place row factor of the split RMSNorm: buf[r, 0:D) *= rsqrt(sum_{g <
  * ngroups} ssq[r * ssq_ld + g] / D + eps) for bf16 rows (row stride ld); the

@@ -1,0 +1,147 @@
+"""Definitions in 64 bits of the attention operators over parts of the sequence, for their tests."""
+import math
+
+import torch
+
+HD = 128
+HALF_STEP = 2.0 ** -8          # bf16 rounding: half a step relative to the value
+DT = torch.float64
+
+
+def numbers(grid, block):
+    return [-(-g // b) for g, b in zip(grid, block)]
+
+
+def volume(d):
+    return d[0] * d[1] * d[2]
+
+
+def block_count(grid, block):
+    return volume(numbers(grid, block))
+
+
+def block_of(grid, block, device="cpu"):
+    """Block of each token, in token order."""
+    n = numbers(grid, block)
+    f, i, j = torch.meshgrid(*(torch.arange(g, device=device) for g in grid), indexing="ij")
+    return (((f // block[0]) * n[1] + i // block[1]) * n[2] + j // block[2]).reshape(-1)
+
+
+def select(q, k, heads, qg, kg, qb, kb, topk, mask=None):
+    """(blocks, counts) by sorting (rank of the mask, score, block) row by row."""
+    B = q.shape[0]
+    nq, nk = block_count(qg, qb), block_count(kg, kb)
+    mine, theirs = block_of(qg, qb), block_of(kg, kb)
+    blocks = torch.full((B, heads, nq, topk), -1, dtype=torch.int32)
+    counts = torch.zeros((B, heads, nq), dtype=torch.int32)
+
+    def means(x, of, n):
+        x = x.cpu().to(DT).reshape(B, -1, heads, HD)
+        out = torch.zeros(B, n, heads, HD, dtype=DT).index_add_(1, of, x)
+        return out / torch.bincount(of, minlength=n).to(DT)[None, :, None, None]
+
+    score = torch.einsum("bihd,bjhd->bhij", means(q, mine, nq), means(k, theirs, nk)).tolist()
+    kind = torch.ones(nq, nk).tolist() if mask is None else mask.cpu().clamp(max=2).tolist()
+    for b in range(B):
+        for h in range(heads):
+            for i in range(nq):
+                row = [(-kind[i][j], 0.0 if kind[i][j] == 2 else (math.inf if math.isnan(s) else -s), j)
+                       for j, s in enumerate(score[b][h][i]) if kind[i][j] > 0]
+                keep = sorted(j for _, _, j in sorted(row)[:topk])
+                blocks[b, h, i, :len(keep)] = torch.tensor(keep, dtype=torch.int32)
+                counts[b, h, i] = len(keep)
+    return blocks, counts
+
+
+def attend(q, k, v, weight):
+    """softmax(q k^T / sqrt(128)) v of one head with whole-number key weights [n, m] (0: not there, 2: listed
+    twice): output, log of the denominator, sum of p |v| (what the rounding of p can move) and the largest sum
+    of |q| |k| (what the fp32 sums of the logits can move)."""
+    logits = q @ k.T / HD ** 0.5
+    logits = torch.where(weight > 0, logits, -math.inf)
+    top = logits.amax(-1, keepdim=True)
+    top = torch.where(top == -math.inf, 0.0, top)
+    p = torch.where(weight > 0, weight * (logits - top).exp(), 0.0)
+    total = p.sum(-1, keepdim=True)
+    p = p / torch.where(total == 0, 1.0, total)
+    size = torch.where(weight > 0, (q.abs() @ k.abs().T) / HD ** 0.5, 0.0).amax(-1)
+    return p @ v, (top + total.log()).squeeze(-1), p @ v.abs(), size
+
+
+def check_attention(out, lse, ref, ref_lse, moved, size):
+    """out (bf16) and lse against the 64-bit values.  Each p is rounded to bf16 once (2^-8 of it) and the output
+    once (2^-8); a logit is a sum of 128 exact products in fp32 (at most 128 roundings of 2^-24 of the sum of
+    their sizes, and the scale's), and moves every p by as much; exp2 and the sums add a few 2^-22."""
+    logit = (130 * 2.0 ** -24) * size
+    bound = HALF_STEP * 1.01 * (moved + ref.abs()) + (2 * logit[..., None] + 2.0 ** -18) * moved + 1e-30
+    off = (out.to(DT) - ref).abs()
+    assert bool((off <= bound).all()), f"largest excess {(off - bound).max().item():.3g}"
+    if lse is not None:
+        none = ref_lse == -math.inf
+        assert torch.equal(lse.to(DT) == -math.inf, none)
+        off = torch.where(none, 0.0, (lse.to(DT) - ref_lse).abs())
+        far = off - (logit + 2.0 ** -18 + 2.0 ** -22 * ref_lse.abs().nan_to_num(0, 0, 0))
+        assert bool((far <= 0).all()), f"lse: largest excess {far.max().item():.3g}"
+
+
+def attention_blocks(q, k, v, heads, qg, kg, qb, kb, blocks, counts):
+    B, dev = q.shape[0], q.device
+    Lq, nk = volume(qg), block_count(kg, kb)
+    mine, theirs = block_of(qg, qb, dev), block_of(kg, kb, dev)
+    o, moved = (torch.zeros(B, Lq, heads * HD, dtype=DT, device=dev) for _ in range(2))
+    lse, size = (torch.zeros(B, heads, Lq, dtype=DT, device=dev) for _ in range(2))
+    there = torch.arange(blocks.shape[-1], device=dev) < counts[..., None]
+    there &= (blocks >= 0) & (blocks < nk)
+    for b in range(B):
+        for h in range(heads):
+            part = slice(h * HD, (h + 1) * HD)
+            weight = torch.zeros(blocks.shape[2], nk + 1, dtype=DT, device=dev)
+            at = torch.where(there[b, h], blocks[b, h], nk).long()
+            weight.scatter_add_(1, at, torch.ones_like(at, dtype=DT))
+            o[b, :, part], lse[b, h], moved[b, :, part], size[b, h] = attend(
+                q[b, :, part].to(DT), k[b, :, part].to(DT).nan_to_num(0, 0, 0), v[b, :, part].to(DT).nan_to_num(0, 0, 0),
+                weight[mine][:, theirs])
+    return o, lse, moved, size.transpose(1, 2).repeat_interleave(HD, -1)
+
+
+def gathered(cache, table, n):
+    """The first n places of a sequence, and whether each is in a page that is there."""
+    page = cache.shape[1]
+    slot = torch.arange(n, device=cache.device)
+    at = table.long()[slot // page]
+    ok = (at >= 0) & (at < cache.shape[0])
+    return torch.where(ok[:, None], cache[at.clamp(0, cache.shape[0] - 1), slot % page].to(DT), 0.0), ok
+
+
+def attention_paged(q, k_cache, v_cache, table, lens, heads):
+    B, T, dev = q.shape[0], q.shape[1], q.device
+    o, moved = (torch.zeros(B, T, heads * HD, dtype=DT, device=dev) for _ in range(2))
+    lse, size = (torch.zeros(B, heads, T, dtype=DT, device=dev) for _ in range(2))
+    for b in range(B):
+        n = min(max(int(lens[b]), 0), table.shape[1] * k_cache.shape[1])
+        k, ok = gathered(k_cache, table[b], n)
+        v, _ = gathered(v_cache, table[b], n)
+        for h in range(heads):
+            part = slice(h * HD, (h + 1) * HD)
+            if n == 0:
+                lse[b, h] = -math.inf
+                continue
+            o[b, :, part], lse[b, h], moved[b, :, part], size[b, h] = attend(
+                q[b, :, part].to(DT), k[:, part], v[:, part], ok.to(DT).expand(T, n))
+    return o, lse, moved, size.transpose(1, 2).repeat_interleave(HD, -1)
+
+
+def rotated(x, slot, heads, hw, gain, eps=1e-6, split=(44, 42, 42), theta=10000.0, rope=True):
+    """x [T, D] (64 bits) normed across heads and turned at the places `slot`; and the size of what each output
+    sums up (|a| + |b| of its pair)."""
+    if gain is not None:
+        x = x / (x.pow(2).mean(-1, keepdim=True) + eps).sqrt() * gain.to(DT)
+    x = x.reshape(-1, heads, HD // 2, 2)
+    size = x.abs().sum(-1, keepdim=True).expand_as(x).reshape(-1, heads * HD)
+    if rope:
+        H, W = hw
+        place = torch.stack((slot // (H * W), slot // W % H, slot % W)).to(DT)
+        angle = torch.cat([place[a][:, None] * theta ** (-torch.arange(0, w, 2, dtype=DT, device=x.device) / w)
+                           for a, w in enumerate(split)], -1)
+        x = torch.view_as_real(torch.view_as_complex(x.contiguous()) * torch.polar(torch.ones_like(angle), angle)[:, None])
+    return x.reshape(-1, heads * HD), size

@@ -37,7 +37,10 @@ SYMBOLS = ["wan_dit_create", "wan_dit_load_weights", "wan_dit_missing_weights", 
            "wan_op_attention_qnorm", "wan_op_rms_apply", "wan_dit_sp_begin", "wan_dit_sp_block_qkv",
            "wan_dit_sp_attention", "wan_dit_sp_block_finish", "wan_dit_sp_end",
            "wan_vae_create", "wan_vae_load_weights", "wan_vae_missing_weights", "wan_vae_decode", "wan_vae_sync",
-           "wan_vae_last_error", "wan_vae_destroy", "wan_op_conv3d", "wan_op_set_gemm_pair", "wan_op_gemm_pair_clusters"]
+           "wan_vae_last_error", "wan_vae_destroy", "wan_op_conv3d", "wan_op_set_gemm_pair", "wan_op_gemm_pair_clusters",
+           "wan_op_block_select", "wan_op_block_select_workspace", "wan_op_attention_blocks",
+           "wan_op_attention_blocks_workspace", "wan_op_kv_append", "wan_op_attention_paged",
+           "wan_op_attention_paged_workspace"]
 
 
 class WanError(RuntimeError):
@@ -62,6 +65,17 @@ class wan_epilogue(C.Structure):
                 ("gain", C.c_void_p), ("ssq", C.c_void_p), ("ssq_ld", C.c_int64), ("norm_cols", C.c_int),
                 ("rope", C.c_int), ("rope_F", C.c_int), ("rope_H", C.c_int), ("rope_W", C.c_int),
                 ("rope_t", C.c_int), ("rope_h", C.c_int), ("rope_w", C.c_int), ("rope_theta", C.c_float)]
+
+
+class wan_block_grid(C.Structure):
+    _fields_ = [(n, C.c_int) for n in ("q_F", "q_H", "q_W", "k_F", "k_H", "k_W",
+                                        "qb_F", "qb_H", "qb_W", "kb_F", "kb_H", "kb_W")]
+
+
+class wan_kv_cache(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("page_stride", C.c_int64), ("token_stride", C.c_int64),
+                ("num_pages", C.c_int), ("page_size", C.c_int), ("table", C.c_void_p), ("table_ld", C.c_int64),
+                ("max_pages", C.c_int)]
 
 
 _lib = None
@@ -126,6 +140,15 @@ def lib() -> C.CDLL:
         "wan_vae_sync": (I, [P, P]),
         "wan_vae_last_error": (C.c_char_p, [P]),
         "wan_vae_destroy": (None, [P]),
+        "wan_op_block_select": (I, [P, I64, P, I64, I, I, C.POINTER(wan_block_grid), P, I, P, P, P, I64, P]),
+        "wan_op_block_select_workspace": (I64, [I, I, C.POINTER(wan_block_grid)]),
+        "wan_op_attention_blocks": (I, [P, I64, P, I64, P, I64, P, I64, I, I, C.POINTER(wan_block_grid), P, P, I, P, P,
+                                        I64, P]),
+        "wan_op_attention_blocks_workspace": (I64, [I, I, C.POINTER(wan_block_grid), I]),
+        "wan_op_kv_append": (I, [P, I64, P, I64, I, I, I, P, P, P, F, I, I, I, I, I, I, F, P, I64, P, P, I64,
+                                 C.POINTER(wan_kv_cache), P]),
+        "wan_op_attention_paged": (I, [P, I64, C.POINTER(wan_kv_cache), P, P, I64, I, I, I, P, P, I64, P]),
+        "wan_op_attention_paged_workspace": (I64, [I, I, I, C.POINTER(wan_kv_cache)]),
         "wan_op_conv3d": (I, [P, P, I, I, I, I, I, I, P, I64, P, I, I, I, I, I, P, I64, P, I64, I, P]),
     }
     for name, (res, args) in sig.items():
@@ -457,6 +480,225 @@ def op_rms_apply(buf_ptr, ld, rows, D, ssq_ptr, ssq_ld, ngroups, eps, stream=Non
 def op_attention_ptr(q, ldq, k, ldk, v, ldv, o, ldo, B, heads, Lq, Lk, stream=None):
     _check(lib().wan_op_attention(q, ldq, k, ldk, v, ldv, o, ldo, B, heads, Lq, Lk, _stream(stream)),
            "wan_op_attention")
+
+
+# ---------------------------------------------------------------- attention over parts of the sequence
+def _rows(name, t, dtype=None):
+    """A [B, L, D] tensor whose samples follow each other (row (b, l) at (b * L + l) * ld): its ld."""
+    import torch
+    if t.dim() != 3 or t.dtype != (dtype or torch.bfloat16) or not t.is_cuda:
+        raise ValueError(f"{name}: a CUDA tensor [B, L, D] of {dtype or torch.bfloat16} is needed, "
+                         f"got {tuple(t.shape)} {t.dtype} on {t.device}")
+    ld = t.stride(1) if t.shape[1] > 1 else t.stride(0) if t.shape[0] > 1 and t.shape[1] == 1 else t.shape[2]
+    if t.stride(2) != 1 or (t.shape[0] > 1 and t.shape[1] > 1 and t.stride(0) != t.shape[1] * ld):
+        raise ValueError(f"{name}: rows must be dense and samples follow each other, got strides {t.stride()}")
+    return ld
+
+
+def _dense(name, t, shape, dtype, device):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name}: a contiguous {dtype} tensor {tuple(shape)} on {device} is needed, "
+                         f"got {tuple(t.shape)} {t.dtype} on {t.device}")
+    return t
+
+
+def _block_grid(q_grid, k_grid, q_block, k_block) -> wan_block_grid:
+    return wan_block_grid(*(int(n) for d in (q_grid, k_grid, q_block, k_block) for n in d))
+
+
+def _blocks_of(grid, block) -> int:
+    n = 1
+    for g, b in zip(grid, block):
+        n *= -(-g // b)
+    return n
+
+
+class _op_device:
+    """The tensors' device and the launch stream made current for a call: buffers that the call allocates
+    belong to the stream that uses them."""
+
+    def __init__(self, device, stream):
+        import torch
+        self._enter = []
+        self._device = device
+        if device.index is not None and device.index != torch.cuda.current_device():
+            self._enter.append(torch.cuda.device(device))
+        if stream is not None:
+            s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+            self._enter.append(torch.cuda.stream(s))
+
+    def __enter__(self):
+        for c in self._enter:
+            c.__enter__()
+        self.stream = _stream()
+        return self
+
+    def __exit__(self, *exc):
+        for c in reversed(self._enter):
+            c.__exit__(*exc)
+
+    def scratch(self, nbytes, given):
+        """The caller's workspace, or a new one."""
+        import torch
+        if given is not None or nbytes <= 0:
+            return given
+        return torch.empty(nbytes, dtype=torch.uint8, device=self._device)
+
+
+def _nbytes(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def op_block_select_workspace(B, heads, q_grid, k_grid, q_block, k_block) -> int:
+    return lib().wan_op_block_select_workspace(B, heads, C.byref(_block_grid(q_grid, k_grid, q_block, k_block)))
+
+
+def op_block_select(q, k, heads, q_grid, k_grid, q_block, k_block, topk, mask=None, blocks=None, counts=None,
+                    workspace=None, stream=None):
+    """The topk best-scored key blocks of each query block (wan_op_block_select): q, k bf16 [B, L, D] (column
+    slices of a packed projection will do), grids and blocks (frames, rows, columns), mask uint8 [query blocks,
+    key blocks] or None.  Returns (blocks int32 [B, heads, query blocks, topk], counts int32 [B, heads, query
+    blocks]).  Buffers that are not given are allocated."""
+    import torch
+    B, nq, nk, dev = q.shape[0], _blocks_of(q_grid, q_block), _blocks_of(k_grid, k_block), q.device
+    ldq, ldk = _rows("q", q), _rows("k", k)
+    _tokens_match("q", q, B, q_grid, heads, dev)
+    _tokens_match("k", k, B, k_grid, heads, dev)
+    if mask is not None:
+        _dense("mask", mask, (nq, nk), torch.uint8, dev)
+    g = _block_grid(q_grid, k_grid, q_block, k_block)
+    with _op_device(dev, stream) as on:
+        if blocks is None:
+            blocks = torch.empty((B, heads, nq, max(topk, 0)), dtype=torch.int32, device=dev)
+        if counts is None:
+            counts = torch.empty((B, heads, nq), dtype=torch.int32, device=dev)
+        _dense("blocks", blocks, (B, heads, nq, topk), torch.int32, dev)
+        _dense("counts", counts, (B, heads, nq), torch.int32, dev)
+        ws = on.scratch(lib().wan_op_block_select_workspace(B, heads, C.byref(g)), workspace)
+        _check(lib().wan_op_block_select(_ptr(q), ldq, _ptr(k), ldk, B, heads, C.byref(g), _ptr(mask), topk, _ptr(blocks),
+                                         _ptr(counts), _ptr(ws), _nbytes(ws), on.stream), "wan_op_block_select")
+    return blocks, counts
+
+
+def _tokens_match(name, t, B, grid, heads, device):
+    if t.shape[0] != B or t.shape[1] != grid[0] * grid[1] * grid[2] or t.shape[2] != heads * 128 or t.device != device:
+        raise ValueError(f"{name}: [{B}, {grid[0] * grid[1] * grid[2]}, {heads * 128}] on {device} is needed, "
+                         f"got {tuple(t.shape)} on {t.device}")
+
+
+def op_attention_blocks_workspace(B, heads, q_grid, k_grid, q_block, k_block, topk) -> int:
+    return lib().wan_op_attention_blocks_workspace(B, heads, C.byref(_block_grid(q_grid, k_grid, q_block, k_block)), topk)
+
+
+def op_attention_blocks(q, k, v, heads, q_grid, k_grid, q_block, k_block, blocks, counts, out=None, lse=None,
+                        workspace=None, stream=None):
+    """Attention of each query block over its listed key blocks (wan_op_attention_blocks): q, k, v bf16 [B, L, D],
+    blocks int32 [B, heads, query blocks, topk], counts int32 [B, heads, query blocks]; lse f32 [B, heads, query
+    tokens] is filled if given.  Returns out, bf16 [B, query tokens, D]."""
+    import torch
+    B, nq, topk, dev = q.shape[0], _blocks_of(q_grid, q_block), blocks.shape[-1], q.device
+    Lq = q_grid[0] * q_grid[1] * q_grid[2]
+    ldq, ldk, ldv = _rows("q", q), _rows("k", k), _rows("v", v)
+    _tokens_match("q", q, B, q_grid, heads, dev)
+    _tokens_match("k", k, B, k_grid, heads, dev)
+    _tokens_match("v", v, B, k_grid, heads, dev)
+    _dense("blocks", blocks, (B, heads, nq, topk), torch.int32, dev)
+    _dense("counts", counts, (B, heads, nq), torch.int32, dev)
+    if lse is not None:
+        _dense("lse", lse, (B, heads, Lq), torch.float32, dev)
+    g = _block_grid(q_grid, k_grid, q_block, k_block)
+    with _op_device(dev, stream) as on:
+        if out is None:
+            out = torch.empty((B, Lq, heads * 128), dtype=torch.bfloat16, device=dev)
+        ldo = _rows("out", out)
+        _tokens_match("out", out, B, q_grid, heads, dev)
+        ws = on.scratch(lib().wan_op_attention_blocks_workspace(B, heads, C.byref(g), topk), workspace)
+        _check(lib().wan_op_attention_blocks(_ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(out), ldo, B, heads, C.byref(g),
+                                             _ptr(blocks), _ptr(counts), topk, _ptr(lse), _ptr(ws), _nbytes(ws), on.stream),
+               "wan_op_attention_blocks")
+    return out
+
+
+def _kv_cache(k_cache, v_cache, table, B) -> wan_kv_cache:
+    import torch
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if t.dim() != 3 or t.dtype != torch.bfloat16 or not t.is_cuda or t.stride(2) != 1:
+            raise ValueError(f"{name}: a CUDA bf16 tensor [pages, page size, D] with dense rows is needed, "
+                             f"got {tuple(t.shape)} {t.dtype}, strides {t.stride()}")
+    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride() or k_cache.device != v_cache.device:
+        raise ValueError("k_cache and v_cache must have one shape, one layout and one device")
+    if table.dim() != 2 or table.dtype != torch.int32 or table.stride(1) != 1 or table.shape[0] != B or \
+            table.device != k_cache.device:
+        raise ValueError(f"page table: an int32 tensor [{B}, pages] on {k_cache.device} is needed, "
+                         f"got {tuple(table.shape)} {table.dtype} on {table.device}")
+    return wan_kv_cache(k=k_cache.data_ptr(), v=v_cache.data_ptr(), page_stride=k_cache.stride(0),
+                        token_stride=k_cache.stride(1), num_pages=k_cache.shape[0], page_size=k_cache.shape[1],
+                        table=table.data_ptr(), table_ld=max(table.stride(0), table.shape[1]), max_pages=table.shape[1])
+
+
+def op_kv_append(k, v, k_cache, v_cache, table, start, heads, frame, count=None, k_gain=None, q=None, q_gain=None,
+                 q_out=None, eps=1e-6, rope=True, split=(44, 42, 42), theta=10000.0, stream=None):
+    """Append T new tokens per sequence to a paged cache (wan_op_kv_append): k, v (and q) bf16 [B, T, D], caches
+    bf16 [pages, page size, D], table int32 [B, pages], start (and count) int32 [B], frame = (rows, columns) of
+    the token grid, gains f32 [D] (None: no norm).  Returns the rotated queries (q_out, by default a new tensor
+    with zero rows past count) or None without q."""
+    import torch
+    B, T, dev, D = k.shape[0], k.shape[1], k.device, heads * 128
+    ldk, ldv = _rows("k", k), _rows("v", v)
+    for name, t in (("k", k), ("v", v), ("q", q), ("q_out", q_out)):
+        if t is not None and (tuple(t.shape) != (B, T, D) or t.device != dev):
+            raise ValueError(f"{name}: [{B}, {T}, {D}] on {dev} is needed, got {tuple(t.shape)} on {t.device}")
+    _dense("start", start, (B,), torch.int32, dev)
+    if count is not None:
+        _dense("count", count, (B,), torch.int32, dev)
+    for name, t in (("k_gain", k_gain), ("q_gain", q_gain)):
+        if t is not None:
+            _dense(name, t, (D,), torch.float32, dev)
+    c = _kv_cache(k_cache, v_cache, table, B)
+    if k_cache.device != dev or k_cache.shape[2] != D:
+        raise ValueError(f"k_cache: rows of {D} on {dev} are needed, got {tuple(k_cache.shape)} on {k_cache.device}")
+    with _op_device(dev, stream) as on:
+        ldq = ldqo = 0
+        if q is not None:
+            if q_out is None:
+                q_out = torch.empty((B, T, D), dtype=torch.bfloat16, device=dev) if count is None else \
+                    torch.zeros((B, T, D), dtype=torch.bfloat16, device=dev)
+            ldq, ldqo = _rows("q", q), _rows("q_out", q_out)
+        _check(lib().wan_op_kv_append(_ptr(k), ldk, _ptr(v), ldv, B, T, heads, _ptr(start), _ptr(count), _ptr(k_gain), eps,
+                                      int(rope), frame[0], frame[1], split[0], split[1], split[2], theta, _ptr(q), ldq,
+                                      _ptr(q_gain), _ptr(q_out) if q is not None else None, ldqo, C.byref(c), on.stream),
+               "wan_op_kv_append")
+    return q_out if q is not None else None
+
+
+def op_attention_paged_workspace(B, heads, T, k_cache, v_cache, table) -> int:
+    return lib().wan_op_attention_paged_workspace(B, heads, T, C.byref(_kv_cache(k_cache, v_cache, table, B)))
+
+
+def op_attention_paged(q, k_cache, v_cache, table, lens, heads, out=None, lse=None, workspace=None, stream=None):
+    """Attention of T new tokens per sequence over its cached places [0, lens[b]) (wan_op_attention_paged): q bf16
+    [B, T, D], caches bf16 [pages, page size, D], table int32 [B, pages], lens int32 [B]; lse f32 [B, heads, T] is
+    filled if given.  Returns out, bf16 [B, T, D]."""
+    import torch
+    B, T, dev = q.shape[0], q.shape[1], q.device
+    ldq = _rows("q", q)
+    c = _kv_cache(k_cache, v_cache, table, B)
+    if q.shape[2] != heads * 128 or k_cache.shape[2] != heads * 128 or k_cache.device != dev:
+        raise ValueError(f"q and the caches need rows of {heads * 128} on one device, got {tuple(q.shape)} on {dev} and "
+                         f"{tuple(k_cache.shape)} on {k_cache.device}")
+    _dense("lens", lens, (B,), torch.int32, dev)
+    if lse is not None:
+        _dense("lse", lse, (B, heads, T), torch.float32, dev)
+    with _op_device(dev, stream) as on:
+        if out is None:
+            out = torch.empty((B, T, heads * 128), dtype=torch.bfloat16, device=dev)
+        ldo = _rows("out", out)
+        if tuple(out.shape) != tuple(q.shape) or out.device != dev:
+            raise ValueError(f"out: {tuple(q.shape)} on {dev} is needed, got {tuple(out.shape)} on {out.device}")
+        ws = on.scratch(lib().wan_op_attention_paged_workspace(B, heads, T, C.byref(c)), workspace)
+        _check(lib().wan_op_attention_paged(_ptr(q), ldq, C.byref(c), _ptr(lens), _ptr(out), ldo, B, heads, T, _ptr(lse),
+                                            _ptr(ws), _nbytes(ws), on.stream), "wan_op_attention_paged")
+    return out
 
 
 def op_layernorm(x, y, eps, mode, gamma=None, beta=None, shift0=None, shift1=None, scale0=None, scale1=None,

@@ -888,6 +888,8 @@ cudaError_t init_kernel_attributes() {
     if (e == cudaSuccess) e = init_gemm_attributes();
     if (e == cudaSuccess) e = init_conv_attributes();
     if (e == cudaSuccess) e = init_layernorm_attributes();
+    if (e == cudaSuccess) e = init_attention_list_attributes();
+    if (e == cudaSuccess) e = init_block_select_attributes();
     return e;
 }
 

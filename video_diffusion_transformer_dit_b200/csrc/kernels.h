@@ -85,7 +85,7 @@ bool make_tmap_3d(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t d1, 
                   uint64_t ld2_elems, uint32_t box_inner, uint32_t box1);
 
 bool make_tmap_5d(CUtensorMap* m, const void* ptr, const uint64_t (&dims)[5], const uint64_t (&strides_elems)[4],
-                  uint32_t box_inner, uint32_t box1, uint32_t box2);
+                  uint32_t box_inner, uint32_t box1, uint32_t box2, uint32_t box3 = 1);
 
 // C = epi(A[M,K] . W[N,K]^T); returns a CUDA error (or cudaErrorInvalidValue
 // for unsupported shapes).
@@ -109,6 +109,65 @@ struct RowNorm {
 cudaError_t launch_attention(const void* q, long long ldq, const void* k, long long ldk, const void* v,
                              long long ldv, void* o, long long ldo, int B, int heads, int Lq, int Lk,
                              const LaunchCtx& ctx, const RowNorm& qn = RowNorm{nullptr, 0, 0, 0.f, 0.f});
+
+// ---------------------------------------------------------------- attention over parts of the sequence
+// Token grids of queries and keys and the boxes of tokens that make their blocks
+// (axes frames, rows, columns; a block at the grid's edge holds fewer tokens).
+struct BlockGrid {
+    int q[3], k[3], qb[3], kb[3];
+    __host__ __device__ int nq(int a) const { return (q[a] + qb[a] - 1) / qb[a]; }
+    __host__ __device__ int nk(int a) const { return (k[a] + kb[a] - 1) / kb[a]; }
+    __host__ __device__ int q_blocks() const { return nq(0) * nq(1) * nq(2); }
+    __host__ __device__ int k_blocks() const { return nk(0) * nk(1) * nk(2); }
+    __host__ __device__ int q_tokens() const { return q[0] * q[1] * q[2]; }
+    __host__ __device__ int k_tokens() const { return k[0] * k[1] * k[2]; }
+    __host__ __device__ int q_volume() const { return qb[0] * qb[1] * qb[2]; }
+    __host__ __device__ int k_volume() const { return kb[0] * kb[1] * kb[2]; }
+};
+
+// Keys and values in pages: page p, token r of it at k + p * page_stride + r *
+// token_stride (elements); sequence b's page number i is table[b * table_ld + i].
+struct KvPages {
+    void* k;
+    void* v;
+    long long page_stride, token_stride;
+    int num_pages, page_size;
+    const int* table;
+    long long table_ld;
+    int max_pages;
+};
+
+// Attention of each query block over the key blocks listed for it (blocks
+// [B, heads, nqb, topk], the first counts[B, heads, nqb] entries of each list;
+// entries outside the key grid are skipped); lse may be null.
+cudaError_t launch_attention_blocks(const void* q, long long ldq, const void* k, long long ldk, const void* v,
+                                    long long ldv, void* o, long long ldo, int B, int heads, const BlockGrid& g,
+                                    const int* blocks, const int* counts, int topk, float* lse, void* ws,
+                                    const LaunchCtx& ctx);
+// Attention of T new tokens per sequence over the first lens[b] tokens of its pages.
+cudaError_t launch_attention_paged(const void* q, long long ldq, const KvPages& c, const int* lens, void* o,
+                                   long long ldo, int B, int heads, int T, float* lse, void* ws, const LaunchCtx& ctx);
+// Bytes of workspace the two need (0: the launch writes its outputs directly); -1: sizes out of range.
+long long attention_blocks_workspace(int B, int heads, const BlockGrid& g, int topk);
+long long attention_paged_workspace(int B, int heads, int T, int max_pages, int page_size);
+cudaError_t init_attention_list_attributes();
+
+// The topk best-scored key blocks of each query block (score: dot product of the
+// blocks' means, fp64), ascending, -1 past counts[]; mask [q blocks, k blocks]
+// (0 never, 1 by score, 2 always) or null.
+cudaError_t launch_block_select(const void* q, long long ldq, const void* k, long long ldk, int B, int heads,
+                                const BlockGrid& g, const uint8_t* mask, int topk, int* blocks, int* counts, void* ws,
+                                const LaunchCtx& ctx);
+long long block_select_workspace(int B, int heads, const BlockGrid& g);
+int block_select_max_blocks();  // key blocks per row at most
+cudaError_t init_block_select_attributes();
+
+// Keys (optionally RMS-normed and rotated) and values of T new tokens per
+// sequence into cache places start[b] + t; q (may be null) likewise into q_out.
+cudaError_t launch_kv_append(const void* k, long long ldk, const void* v, long long ldv, int B, int T, int heads,
+                             const int* start, const int* count, const float* k_gain, float eps, int rope, int H, int W,
+                             int rope_t, int rope_h, int rope_w, double theta, const void* q, long long ldq,
+                             const float* q_gain, void* q_out, long long ldqo, const KvPages& c, const LaunchCtx& ctx);
 
 // buf[r, 0:D) *= the RMSNorm row factor of rn (in place, bf16, one rounding).
 cudaError_t launch_rms_apply(void* buf, long long ld, int rows, int D, const RowNorm& rn, const LaunchCtx& ctx);

@@ -10,6 +10,7 @@
 #include <cmath>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <map>
 #include <mutex>
 #include <set>
@@ -1405,6 +1406,136 @@ wan_status wan_op_attention(const void* q, int64_t ldq, const void* k, int64_t l
     LaunchCtx ctx;
     if (!op_ctx(reinterpret_cast<cudaStream_t>(stream), &ctx)) return WAN_ECUDA;
     return op_status(wan::launch_attention(q, ldq, k, ldk, v, ldv, o, ldo, B, heads, Lq, Lk, ctx));
+}
+
+// ---------------------------------------------------------------- attention over parts of the sequence
+namespace {
+bool aligned16(std::initializer_list<const void*> ptrs) {
+    uintptr_t all = 0;
+    for (const void* q : ptrs) all |= reinterpret_cast<uintptr_t>(q);
+    return (all & 15) == 0;
+}
+
+bool ld_ok(int64_t ld, int heads) { return ld >= 128ll * heads && ld % 8 == 0 && ld < (1ll << 31); }
+
+bool group_ok(int64_t n) { return n == 16 || n == 32 || n == 64 || n == 128; }
+
+// Sizes of a block grid within the limits (B, heads included); fills *out.
+bool block_grid_ok(const wan_block_grid* g, int B, int heads, wan::BlockGrid* out) {
+    *out = wan::BlockGrid{{g->q_F, g->q_H, g->q_W}, {g->k_F, g->k_H, g->k_W},
+                          {g->qb_F, g->qb_H, g->qb_W}, {g->kb_F, g->kb_H, g->kb_W}};
+    if (B < 0 || heads <= 0 || (int64_t)B * heads > 65535) return false;
+    int64_t lq = 1, lk = 1, vq = 1, vk = 1;
+    for (int a = 0; a < 3; ++a) {
+        if (out->q[a] < 1 || out->k[a] < 1 || out->qb[a] < 1 || out->kb[a] < 1) return false;
+        if ((lq *= out->q[a]) > (1 << 30) || (lk *= out->k[a]) > (1 << 30) || (vq *= out->qb[a]) > 128 ||
+            (vk *= out->kb[a]) > 128)
+            return false;
+    }
+    return group_ok(vk) && (int64_t)std::max(B, 1) * std::max(lq, lk) <= (1ll << 31);
+}
+
+bool kv_cache_ok(const wan_kv_cache* c, int heads, wan::KvPages* out) {
+    *out = wan::KvPages{c->k, c->v, c->page_stride, c->token_stride, c->num_pages, c->page_size, c->table, c->table_ld, c->max_pages};
+    if (!group_ok(c->page_size) || c->num_pages < 1 || c->max_pages < 1 || c->table_ld < c->max_pages) return false;
+    if ((int64_t)c->max_pages * c->page_size > (1 << 30)) return false;
+    if (!ld_ok(c->token_stride, heads) || c->page_stride % 8 || c->page_stride >= (1ll << 38)) return false;
+    if (c->page_stride < (c->page_size - 1) * c->token_stride + 128ll * heads) return false;
+    return aligned16({c->k, c->v});
+}
+}  // namespace
+
+int64_t wan_op_block_select_workspace(int B, int heads, const wan_block_grid* g) {
+    wan::BlockGrid bg;
+    if (!g || !block_grid_ok(g, B, heads, &bg)) return -1;
+    return wan::block_select_workspace(B, heads, bg);
+}
+
+wan_status wan_op_block_select(const void* q, int64_t ldq, const void* k, int64_t ldk, int B, int heads,
+                               const wan_block_grid* g, const uint8_t* mask, int topk, int32_t* blocks, int32_t* counts,
+                               void* workspace, int64_t workspace_bytes, void* stream) {
+    if (!q || !k || !g || !blocks || !counts || !workspace) return WAN_EINVAL;
+    wan::BlockGrid bg;
+    if (!block_grid_ok(g, B, heads, &bg) || !ld_ok(ldq, heads) || !ld_ok(ldk, heads) || !aligned16({q, k, workspace}))
+        return WAN_ESHAPE;
+    const int nk = bg.k_blocks(), nq = bg.q_blocks();
+    if (topk < 1 || topk > nk || nk > wan::block_select_max_blocks() || nq > 65535 * 32) return WAN_ESHAPE;
+    if (workspace_bytes < wan::block_select_workspace(B, heads, bg)) return WAN_ESHAPE;
+    if (B == 0) return WAN_OK;
+    LaunchCtx ctx;
+    if (!op_ctx(reinterpret_cast<cudaStream_t>(stream), &ctx)) return WAN_ECUDA;
+    return op_status(wan::launch_block_select(q, ldq, k, ldk, B, heads, bg, mask, topk, blocks, counts, workspace, ctx));
+}
+
+int64_t wan_op_attention_blocks_workspace(int B, int heads, const wan_block_grid* g, int topk) {
+    wan::BlockGrid bg;
+    if (!g || topk < 1 || !block_grid_ok(g, B, heads, &bg)) return -1;
+    return wan::attention_blocks_workspace(B, heads, bg, topk);
+}
+
+wan_status wan_op_attention_blocks(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                                   void* o, int64_t ldo, int B, int heads, const wan_block_grid* g, const int32_t* blocks,
+                                   const int32_t* counts, int topk, float* lse, void* workspace, int64_t workspace_bytes,
+                                   void* stream) {
+    if (!q || !k || !v || !o || !g || !blocks || !counts) return WAN_EINVAL;
+    wan::BlockGrid bg;
+    if (topk < 1 || !block_grid_ok(g, B, heads, &bg)) return WAN_ESHAPE;
+    if (!ld_ok(ldq, heads) || !ld_ok(ldk, heads) || !ld_ok(ldv, heads) || !ld_ok(ldo, heads) ||
+        !aligned16({q, k, v, o, workspace}))
+        return WAN_ESHAPE;
+    const int64_t need = wan::attention_blocks_workspace(B, heads, bg, topk);
+    if (need < 0) return WAN_ESHAPE;
+    if (need > 0 && !workspace) return WAN_EINVAL;
+    if (need > 0 && workspace_bytes < need) return WAN_ESHAPE;
+    if (B == 0) return WAN_OK;
+    LaunchCtx ctx;
+    if (!op_ctx(reinterpret_cast<cudaStream_t>(stream), &ctx)) return WAN_ECUDA;
+    return op_status(wan::launch_attention_blocks(q, ldq, k, ldk, v, ldv, o, ldo, B, heads, bg, blocks, counts, topk, lse,
+                                                  workspace, ctx));
+}
+
+wan_status wan_op_kv_append(const void* k, int64_t ldk, const void* v, int64_t ldv, int B, int T, int heads,
+                            const int32_t* start, const int32_t* count, const float* k_gain, float eps, int rope, int H,
+                            int W, int rope_t, int rope_h, int rope_w, float theta, const void* q, int64_t ldq,
+                            const float* q_gain, void* q_out, int64_t ldqo, const wan_kv_cache* cache, void* stream) {
+    if (!k || !v || !start || !cache || !cache->k || !cache->v || !cache->table || (q && !q_out)) return WAN_EINVAL;
+    wan::KvPages pages;
+    if (B < 0 || T < 0 || heads <= 0 || heads > (1 << 20) || (int64_t)B * T > (1ll << 31) || !kv_cache_ok(cache, heads, &pages))
+        return WAN_ESHAPE;
+    if (!ld_ok(ldk, heads) || !ld_ok(ldv, heads) || (q && (!ld_ok(ldq, heads) || !ld_ok(ldqo, heads)))) return WAN_ESHAPE;
+    if (!aligned16({k, v, q, q ? q_out : nullptr, k_gain, q_gain})) return WAN_ESHAPE;
+    if (rope && (H <= 0 || W <= 0 || (int64_t)H * W > (1 << 30) || rope_t < 0 || rope_h < 0 || rope_w < 0 || rope_t % 2 ||
+                 rope_h % 2 || rope_w % 2 || rope_t + rope_h + rope_w != 128 || !(theta > 0.f)))
+        return WAN_ESHAPE;
+    if (B == 0 || T == 0) return WAN_OK;
+    LaunchCtx ctx;
+    if (!op_ctx(reinterpret_cast<cudaStream_t>(stream), &ctx)) return WAN_ECUDA;
+    return op_status(wan::launch_kv_append(k, ldk, v, ldv, B, T, heads, start, count, k_gain, eps, rope, H, W, rope_t, rope_h,
+                                           rope_w, theta, q, ldq, q_gain, q_out, ldqo, pages, ctx));
+}
+
+int64_t wan_op_attention_paged_workspace(int B, int heads, int T, const wan_kv_cache* cache) {
+    wan::KvPages pages;
+    if (!cache || B < 0 || heads <= 0 || T < 0 || (int64_t)B * T > (1ll << 30) || (int64_t)B * heads > (1 << 20) ||
+        !kv_cache_ok(cache, heads, &pages))
+        return -1;
+    return wan::attention_paged_workspace(B, heads, T, pages.max_pages, pages.page_size);
+}
+
+wan_status wan_op_attention_paged(const void* q, int64_t ldq, const wan_kv_cache* cache, const int32_t* lens, void* o,
+                                  int64_t ldo, int B, int heads, int T, float* lse, void* workspace,
+                                  int64_t workspace_bytes, void* stream) {
+    if (!q || !o || !lens || !cache || !cache->k || !cache->v || !cache->table) return WAN_EINVAL;
+    const int64_t need = wan_op_attention_paged_workspace(B, heads, T, cache);
+    if (need < 0 || !ld_ok(ldq, heads) || !ld_ok(ldo, heads) || !aligned16({q, o, workspace})) return WAN_ESHAPE;
+    if (need > 0 && !workspace) return WAN_EINVAL;
+    if (need > 0 && workspace_bytes < need) return WAN_ESHAPE;
+    if (B == 0 || T == 0) return WAN_OK;
+    wan::KvPages pages;
+    kv_cache_ok(cache, heads, &pages);
+    LaunchCtx ctx;
+    if (!op_ctx(reinterpret_cast<cudaStream_t>(stream), &ctx)) return WAN_ECUDA;
+    return op_status(wan::launch_attention_paged(q, ldq, pages, lens, o, ldo, B, heads, T, lse, workspace, ctx));
 }
 
 wan_status wan_op_layernorm(const void* x, void* y, int rows, int D, float eps, int mode, const float* gamma,
