@@ -498,16 +498,16 @@ def test_two_streams_at_once_and_repeats_give_the_same_bits():
 
 @pytest.mark.parametrize("mode", ["blocks", "pages"])
 def test_zero_wait_limit_reports_and_recovers(mode):
-    heads = 2
+    heads = 12                                      # more units than streams: some waits last a unit's time
     if mode == "blocks":
         g, b = (1, 1, 1500), (1, 1, 128)
-        q, k, v = packed(1, 1500, heads, 91)
-        blocks, counts = lists(1, heads, 12, 12, 9, 92, False)
+        q, k, v = packed(3, 1500, heads, 91)
+        blocks, counts = lists(3, heads, 12, 12, 9, 92, False)
         run = lambda: B().op_attention_blocks(q, k, v, heads, g, g, b, b, blocks, counts)  # noqa: E731
     else:
-        kc, vc, table = cache(2, 400, 32, heads, 93)
-        q = rnd((2, 300, heads * 128), 94)
-        ln = torch.tensor([12711, 7000], dtype=torch.int32, device="cuda")
+        kc, vc, table = cache(3, 100, 32, heads, 93)
+        q = rnd((3, 1100, heads * 128), 94)
+        ln = torch.tensor([3111, 1700, 3200], dtype=torch.int32, device="cuda")
         run = lambda: B().op_attention_paged(q, kc, vc, table, ln, heads)  # noqa: E731
     clean = run()
     B().op_sync()

@@ -5,23 +5,33 @@
 //   pages   the T new tokens of each sequence attend to the sequence's cached
 //           keys and values, which lie in pages of 16..128 tokens.
 // Both are the same loop: a list of token groups, gathered by TMA into tiles of
-// 128 keys, softmax with a running maximum and sum, O += P V per tile.
+// 64 keys (a block or page of 128 tokens is two groups), softmax with a running
+// maximum and sum, O += P V per tile.
 //
 // A work unit is one query tile (up to 128 rows of one head and sample) and one
 // split of its list.  A CTA (one per SM) carries two units side by side
-// (streams t = 0, 1), each with its own Q tile, S_t, P_t (over S_t) and O_t in
-// tensor memory, so one stream's exponentials overlap the other's MMAs although
-// the two read different keys.  In step k of its unit a stream issues
-// S(k) = Q K_k^T and then O += P(k-1) V_(k-1); the streams alternate step by
-// step, and their K and V tiles pass through one ring of five 32 KB slots in
-// that order.  Streams walk units blockIdx.x * 2 + t, + 2 * gridDim.x, ...
+// (streams t = 0, 1), each with its own Q tile, so one stream's exponentials
+// overlap the other's MMAs although the two read different keys.  A stream has
+// 256 columns of tensor memory: O_t (128) and two S buffers of 64 columns, each
+// overwritten by its P (bf16, 32 columns).  In step k of its unit a stream issues
+// S(k) = Q K_k^T into the one buffer and O += P(k-1) V_(k-1) from the other, so
+// the softmax finds S(k) finished when it is done with tile k - 1 (with one
+// 128-key S per stream the softmax and the MMAs of a stream took turns: 1.3
+// times the time).  The streams share nothing but the SM: each has its producer,
+// its issuer, its softmax warps and its ring of five 16 KB slots for K and V tiles
+// in the order K(k), V(k - 1).  Stream t walks units blockIdx.x * 2 + t,
+// + 2 * gridDim.x, ...
+//
+// Every barrier that advances once per tile exists once per S buffer: a waiting
+// warp is then at most one phase behind (S(k) is issued after P.V of tile k - 2,
+// which waits for the P of tile k - 2), so the phase's parity names it.
 //
 // Warps (registers per thread as in the dense kernel):
-//   0      TMA producer (whole warp: each lane gathers one token group of the
-//          tile) and the 128-bit mask of the tile's keys;
-//   1      tensor-memory owner and MMA issuer; it also zeroes the V rows of a tile
-//          past the sequence's end inside a page before the tile's P.V;
-//   2..3   idle;
+//   0, 2   TMA producer of stream 0 / 1 and the 64-bit mask of each tile's keys (one
+//          producer for both streams was the bottleneck: gathering a tile takes it
+//          about as long as the tile's MMAs);
+//   1, 3   MMA issuer of stream 0 / 1 (1 owns the tensor memory); it also zeroes the
+//          V rows of a tile past the sequence's end inside a page before its P.V;
 //   4..11  softmax of stream 0 / 1, one query row per thread; warps without a
 //          row only keep the barriers' counts.
 // Where there are too few query tiles to fill the GPU, lists are split: each
@@ -33,15 +43,18 @@
 namespace wan {
 
 namespace alist {
-constexpr int TILE_BYTES = 128 * 128 * 2;  // 128 rows x 128 columns: two 64-column swizzled halves
-constexpr int HALF_BYTES = 128 * 128;
-constexpr int SLOTS = 5;
-constexpr int MASKS = 8;                   // key masks per stream (tiles in flight: at most 4)
+constexpr int KEYS = 64;                   // keys per tile
+constexpr int Q_BYTES = 128 * 128 * 2;     // 128 rows x 128 columns: two 64-column swizzled halves
+constexpr int Q_HALF = 128 * 128;
+constexpr int SLOT_BYTES = KEYS * 128 * 2; // a K or V tile: two 64-column halves
+constexpr int KV_HALF = KEYS * 128;
+constexpr int SLOTS = 5;                   // per stream
+constexpr int MASKS = 16;                  // key masks per stream (tiles in flight: at most 6)
 constexpr int SQ = 0;
-constexpr int SKV = SQ + 2 * TILE_BYTES;
-constexpr int SMASK = SKV + SLOTS * TILE_BYTES;
-constexpr int SBAR = SMASK + 2 * MASKS * 16;
-constexpr int SMEM_BYTES = SBAR + 256 + 1024;
+constexpr int SKV = SQ + 2 * Q_BYTES;
+constexpr int SMASK = SKV + 2 * SLOTS * SLOT_BYTES;
+constexpr int SBAR = SMASK + 2 * MASKS * 8;
+constexpr int SMEM_BYTES = SBAR + 320 + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
 constexpr int THREADS = 384;
 constexpr int REGS_LAUNCH = 168;
@@ -53,12 +66,25 @@ constexpr int PLAN_SMS = 148;              // SMs the split plan assumes
 enum Mode { BLOCKS, PAGES };
 }  // namespace alist
 
+// n / d for n < 2^31 by a multiplication: the producers decode block numbers, and
+// a division is a long dependent sequence for a warp that shares its scheduler.
+struct FastDiv {
+    uint32_t mul, shift;
+    __device__ __forceinline__ int operator()(int n) const {
+        return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift);
+    }
+};
+
 struct ListParams {
     int units, splits, nqb, heads, B;
     int rows;               // rows of a full query tile
-    int E, log_group;       // token groups per tile, log2 of tokens per group
+    int E, log_group;       // token groups per tile, log2 of tokens per group (at most 64)
+    int log_sub;            // log2 of groups per block or page (1 for 128 tokens)
     // blocks
     BlockGrid g;
+    int sub[3], step[3];    // box of one group; offset of a block's second group
+    int nk1, nk2;           // key blocks along rows and columns
+    FastDiv by_nk2, by_nk1;
     const int* blocks;
     const int* counts;
     int topk, nkb;
@@ -97,12 +123,12 @@ __device__ __forceinline__ ListUnit list_unit(const ListParams& p, int u) {
     int tiles;
     if (MODE == alist::BLOCKS) {
         const int c = __ldg(p.counts + ((long long)x.b * p.heads + x.h) * p.nqb + x.qt);
-        x.length = min(max(c, 0), p.topk);
+        x.length = min(max(c, 0), p.topk) << p.log_sub;
         tiles = (x.length + p.E - 1) / p.E;
     } else {
-        const int cap = p.max_pages << p.log_group;
+        const int cap = p.max_pages << (p.log_group + p.log_sub);
         x.length = min(max(__ldg(p.lens + x.b), 0), cap);
-        tiles = (x.length + 127) >> 7;
+        tiles = (x.length + alist::KEYS - 1) / alist::KEYS;
     }
     x.j0 = (int)((long long)tiles * s / p.splits);
     const int j1 = (int)((long long)tiles * (s + 1) / p.splits);
@@ -111,33 +137,61 @@ __device__ __forceinline__ ListUnit list_unit(const ListParams& p, int u) {
     return x;
 }
 
-// The interleaved walk that producer and issuer share: step k
-// of a unit loads K(k) (k < n) and V(k - 1) (k > 0); empty units have no step.
+// Units of one stream that have tiles: next() takes the next one (false: none left).
 template <alist::Mode MODE>
 struct ListWalk {
     ListUnit x;
-    int u, k;
-    __device__ __forceinline__ void start(const ListParams& p, int t) {
-        u = blockIdx.x * 2 + t - 2 * gridDim.x;
-        next(p);
-    }
-    __device__ __forceinline__ void next(const ListParams& p) {
-        k = 0;
+    int u;
+    __device__ __forceinline__ explicit ListWalk(int t) : u(blockIdx.x * 2 + t - 2 * gridDim.x) {}
+    __device__ __forceinline__ bool next(const ListParams& p) {
         do {
             u += 2 * gridDim.x;
-            if (u >= p.units) return;
+            if (u >= p.units) return false;
             x = list_unit<MODE>(p, u);
+            // read by every lane alike, but known to the compiler as warp-uniform only from
+            // a broadcast: ring slots and descriptors that follow from it stay in uniform registers
+            x.n = __shfl_sync(0xffffffffu, x.n, 0);
         } while (x.n == 0);
+        return true;
     }
-    __device__ __forceinline__ bool live(const ListParams& p) const { return u < p.units; }
 };
 
-// Origin of a token group: block (f, i, j) or page number (in f); out-of-range
-// batch / page coordinates where there is none (TMA fills zeros).
+// Query token of row r of query tile qt, -1 where the tile has no such row.
+template <alist::Mode MODE>
+__device__ __forceinline__ int list_token(const ListParams& p, int qt, int r) {
+    if (MODE == alist::PAGES) return qt * 128 + r < p.T ? qt * 128 + r : -1;
+    const int nj = p.g.nq(2), ni = p.g.nq(1);
+    const int f = (qt / nj / ni) * p.g.qb[0] + r / (p.g.qb[2] * p.g.qb[1]);
+    const int i = (qt / nj % ni) * p.g.qb[1] + r / p.g.qb[2] % p.g.qb[1];
+    const int j = (qt % nj) * p.g.qb[2] + r % p.g.qb[2];
+    return r < p.rows && f < p.g.q[0] && i < p.g.q[1] && j < p.g.q[2] ? (f * p.g.q[1] + i) * p.g.q[2] + j : -1;
+}
+
+// Origin of a token group; an out-of-range sample or page where there is none
+// (TMA fills zeros).
 struct ListGroup {
-    int f, i, j, b;
+    int f, i, j, b;  // blocks: token coordinates and sample; pages: first place, row in the page, -, page
     bool ok;
 };
+
+// mbar_spin by a whole warp: one probe and one vote where the phase is complete
+// (the usual case), no divergence.
+__device__ __forceinline__ bool warp_spin(uint64_t* bar, uint32_t parity, volatile int* abort, const WaitCtl& wc) {
+    if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
+    const uint64_t t0 = global_ns();
+    for (uint32_t n = 1;; ++n) {
+        if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
+        if ((n & 63) == 0 || wc.limit_ns == 0) {
+            const bool late = wc.limit_ns == 0 || global_ns() - t0 > wc.limit_ns;
+            if (__any_sync(0xffffffffu, late || *abort)) {
+                if (!*abort && wc.err) atomicExch(wc.err, ERR_TIMEOUT);
+                *abort = 1;
+                __syncwarp();
+                return false;
+            }
+        }
+    }
+}
 
 template <alist::Mode MODE>
 __global__ void __launch_bounds__(alist::THREADS, 1)
@@ -146,19 +200,17 @@ __global__ void __launch_bounds__(alist::THREADS, 1)
     using namespace alist;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint4* masks = reinterpret_cast<uint4*>(smem + SMASK);  // [2][MASKS]
+    uint2* masks = reinterpret_cast<uint2*>(smem + SMASK);  // [2][MASKS]
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SBAR);
     uint64_t* q_full = bars;                 // [2]
     uint64_t* q_empty = q_full + 2;          // [2] the unit's last S has read Q
-    uint64_t* kv_full = q_empty + 2;         // [SLOTS]
-    uint64_t* kv_empty = kv_full + SLOTS;    // [SLOTS]
-    uint64_t* s_full = kv_empty + SLOTS;     // [2]
-    uint64_t* s_read = s_full + 2;           // [2] the softmax has read S_t
-    uint64_t* p_part = s_read + 2;           // [2] P of keys 0..63 stored
-    uint64_t* p_full = p_part + 2;           // [2]
-    uint64_t* o_final = p_full + 2;          // [2]
-    uint64_t* drain = o_final + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    uint64_t* kv_full = q_empty + 2;         // [2][SLOTS]
+    uint64_t* kv_empty = kv_full + 2 * SLOTS;  // [2][SLOTS]
+    uint64_t* s_full = kv_empty + 2 * SLOTS; // [2][2] stream, S buffer
+    uint64_t* p_full = s_full + 4;           // [2][2] P stored over S
+    uint64_t* pv_done = p_full + 4;          // [2][2] P.V of the buffer's tile has landed
+    uint64_t* drain = pv_done + 4;           // [2]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5;
@@ -168,17 +220,18 @@ __global__ void __launch_bounds__(alist::THREADS, 1)
         for (int t = 0; t < 2; ++t) {
             mbar_init(q_full + t, 1);
             mbar_init(q_empty + t, 1);
-            mbar_init(s_full + t, 1);
-            mbar_init(s_read + t, 4);
-            mbar_init(p_part + t, 4);
-            mbar_init(p_full + t, 4);
-            mbar_init(o_final + t, 1);
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(s_full + 2 * t + i, 1);
+                mbar_init(p_full + 2 * t + i, 4);
+                mbar_init(pv_done + 2 * t + i, 1);
+            }
         }
-        for (int s = 0; s < SLOTS; ++s) {
+        for (int s = 0; s < 2 * SLOTS; ++s) {
             mbar_init(kv_full + s, 1);
             mbar_init(kv_empty + s, 1);
         }
         mbar_init(drain, 1);
+        mbar_init(drain + 1, 1);
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tmQ);
@@ -192,63 +245,69 @@ __global__ void __launch_bounds__(alist::THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    // producer: slots with a load issued and the phase it completes; Q phases;
-    // issuer: whether any MMA went out (both drained after an abort, before exit)
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+    // producer: slots with a load issued and the phase it completes, phase of the
+    // last Q load; issuer: whether any MMA went out (both drained after an abort)
     uint32_t armed = 0, par = 0;
-    int qpar[2] = {-1, -1};
+    int qpar = -1;
     bool issued = false;
 
     if (warp < 4) {
         regs_dealloc<REGS_CONTROL>();
-        if (warp == 0) {
-            // ---------------- producer ----------------
+        const int t = warp >> 1;
+        uint8_t* ring = smem + SKV + t * SLOTS * SLOT_BYTES;
+        uint64_t* full = kv_full + t * SLOTS;
+        uint64_t* empty = kv_empty + t * SLOTS;
+        if ((warp & 1) == 0) {
+            // ---------------- producer of stream t ----------------
             auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-                int r = 1;
-                if (lane == 0) r = mbar_wait(bar, parity, abort_flag, p.wc) ? 1 : 0;
-                return __shfl_sync(0xffffffffu, r, 0) != 0;
+                return warp_spin(bar, parity, abort_flag, p.wc);
             };
             const int group = 1 << p.log_group;
-            // place of the lane's four key columns inside their group
-            int off[4];
+            // place of the lane's two key columns inside their group
+            int off[2];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < 2; ++c) {
                 const int r = (c * 32 + lane) & (group - 1);
                 off[c] = r;
                 if (MODE == BLOCKS) {
-                    const int dj = r % p.g.kb[2], di = (r / p.g.kb[2]) % p.g.kb[1], df = r / (p.g.kb[2] * p.g.kb[1]);
+                    const int dj = r % p.sub[2], di = (r / p.sub[2]) % p.sub[1], df = r / (p.sub[2] * p.sub[1]);
                     off[c] = df | di << 8 | dj << 16;
                 }
             }
-            auto group_at = [&](const ListUnit& x, int j) -> ListGroup {  // lane e: group e of tile j
+            // lane e: the list's entry for group e of tile j (bounded by the list's room:
+            // the load does not wait for its length), and the group it names
+            auto fetch = [&](const ListUnit& x, int j) -> int {
+                const int idx = (j * p.E + lane) >> p.log_sub;
+                if (lane >= p.E || idx >= (MODE == BLOCKS ? p.topk : p.max_pages)) return -1;
+                return MODE == BLOCKS
+                           ? __ldg(p.blocks + (((long long)x.b * p.heads + x.h) * p.nqb + x.qt) * p.topk + idx)
+                           : __ldg(p.table + (long long)x.b * p.table_ld + idx);
+            };
+            auto group_of = [&](const ListUnit& x, int j, int id) -> ListGroup {
                 ListGroup o{0, 0, 0, MODE == BLOCKS ? p.B : p.num_pages, false};
                 const int idx = j * p.E + lane;
-                if (lane >= p.E) return o;
                 if (MODE == BLOCKS) {
-                    if (idx >= x.length) return o;
-                    const int id = __ldg(p.blocks + (((long long)x.b * p.heads + x.h) * p.nqb + x.qt) * p.topk + idx);
-                    if (id < 0 || id >= p.nkb) return o;
-                    const int nj = p.g.nk(2), ni = p.g.nk(1);
-                    const int r = id / nj;
-                    o.j = (id - r * nj) * p.g.kb[2];
-                    o.i = (r % ni) * p.g.kb[1];
-                    o.f = (r / ni) * p.g.kb[0];
+                    if (idx >= x.length || id < 0 || id >= p.nkb) return o;
+                    const int r = p.by_nk2(id), f = p.by_nk1(r);
+                    const int second = idx & ((1 << p.log_sub) - 1);
+                    o.j = (id - r * p.nk2) * p.g.kb[2] + second * p.step[2];
+                    o.i = (r - f * p.nk1) * p.g.kb[1] + second * p.step[1];
+                    o.f = f * p.g.kb[0] + second * p.step[0];
                     o.b = x.b;
-                    o.ok = true;
                 } else {
-                    if ((idx << p.log_group) >= x.length) return o;
-                    const int page = __ldg(p.table + (long long)x.b * p.table_ld + idx);
-                    if (page < 0 || page >= p.num_pages) return o;
-                    o.b = page;
-                    o.f = idx << p.log_group;  // first token
-                    o.ok = true;
+                    if ((idx << p.log_group) >= x.length || id < 0 || id >= p.num_pages) return o;
+                    o.b = id;
+                    o.f = idx << p.log_group;
+                    o.i = (idx & ((1 << p.log_sub) - 1)) << p.log_group;
                 }
+                o.ok = true;
                 return o;
             };
-            auto write_mask = [&](const ListUnit& x, const ListGroup& o, uint4* dst) {
-                uint32_t w[4];
+            auto write_mask = [&](const ListUnit& x, const ListGroup& o, uint2* dst) {
+                uint32_t w[2];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < 2; ++c) {
                     const int e = (c * 32 + lane) >> p.log_group;
                     const bool ok = __shfl_sync(0xffffffffu, (int)o.ok, e) != 0;
                     const int f = __shfl_sync(0xffffffffu, o.f, e);
@@ -262,173 +321,154 @@ __global__ void __launch_bounds__(alist::THREADS, 1)
                     }
                     w[c] = __ballot_sync(0xffffffffu, in);
                 }
-                if (lane == 0) *dst = make_uint4(w[0], w[1], w[2], w[3]);
+                if (lane == 0) *dst = make_uint2(w[0], w[1]);
             };
             int c = 0;  // loads so far
             auto load = [&](const CUtensorMap* tm, const ListUnit& x, const ListGroup& o) -> bool {
                 const int slot = c % SLOTS;
                 const uint32_t phase = (c / SLOTS) & 1;
                 ++c;
-                if (!wait(kv_empty + slot, phase ^ 1)) return false;
-                if (lane == 0) mbar_expect_tx(kv_full + slot, TILE_BYTES);
+                if (!wait(empty + slot, phase ^ 1)) return false;
+                if (elect_one()) mbar_expect_tx(full + slot, SLOT_BYTES);
                 __syncwarp();
-                if (lane < p.E) {
-                    uint8_t* dst = smem + SKV + slot * TILE_BYTES + (lane << p.log_group) * 128;
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        if (MODE == BLOCKS)
-                            tma_load_5d(dst + half * HALF_BYTES, tm, kv_full + slot, x.h * 128 + half * 64, o.j, o.i, o.f, o.b);
-                        else
-                            tma_load_3d(dst + half * HALF_BYTES, tm, kv_full + slot, x.h * 128 + half * 64, 0, o.b);
+                const int h0 = x.h * 128;
+                for (int e = 0; e < p.E; ++e) {  // coordinates broadcast: one lane issues from uniform registers
+                    uint8_t* dst = ring + slot * SLOT_BYTES + (e << p.log_group) * 128;
+                    const int f = __shfl_sync(0xffffffffu, o.f, e), i = __shfl_sync(0xffffffffu, o.i, e);
+                    const int b = __shfl_sync(0xffffffffu, o.b, e);
+                    if (MODE == BLOCKS) {
+                        const int j = __shfl_sync(0xffffffffu, o.j, e);
+                        if (elect_one()) {
+                            tma_load_5d(dst, tm, full + slot, h0, j, i, f, b);
+                            tma_load_5d(dst + KV_HALF, tm, full + slot, h0 + 64, j, i, f, b);
+                        }
+                    } else if (elect_one()) {
+                        tma_load_3d(dst, tm, full + slot, h0, i, b);
+                        tma_load_3d(dst + KV_HALF, tm, full + slot, h0 + 64, i, b);
                     }
+                    __syncwarp();
                 }
                 armed |= 1u << slot;
                 par = (par & ~(1u << slot)) | phase << slot;
                 return true;
             };
-            ListWalk<MODE> w[2];
-            ListGroup last[2];   // the previous tile's groups: its V goes one step after its K
-            int tiles[2] = {0, 0}, unit[2] = {0, 0};
-            bool ok = true;
-            for (int t = 0; t < 2; ++t) w[t].start(p, t);
-            while (ok && (w[0].live(p) || w[1].live(p))) {
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (!ok || !w[t].live(p)) continue;
-                    const int k = w[t].k;
-                    if (k == 0) {
-                        if (!wait(q_empty + t, (unit[t] & 1) ^ 1)) { ok = false; continue; }
-                        if (lane == 0) {
-                            uint8_t* dst = smem + SQ + t * TILE_BYTES;
-                            const int h0 = w[t].x.h * 128;
-                            if (MODE == BLOCKS) {
-                                const int nj = p.g.nq(2), ni = p.g.nq(1), qt = w[t].x.qt;
-                                const int j = (qt % nj) * p.g.qb[2], i = (qt / nj % ni) * p.g.qb[1], f = (qt / nj / ni) * p.g.qb[0];
-                                mbar_expect_tx(q_full + t, p.rows * 256);
-                                tma_load_5d(dst, &tmQ, q_full + t, h0, j, i, f, w[t].x.b);
-                                tma_load_5d(dst + HALF_BYTES, &tmQ, q_full + t, h0 + 64, j, i, f, w[t].x.b);
-                            } else {
-                                mbar_expect_tx(q_full + t, TILE_BYTES);
-                                tma_load_3d(dst, &tmQ, q_full + t, h0, w[t].x.qt * 128, w[t].x.b);
-                                tma_load_3d(dst + HALF_BYTES, &tmQ, q_full + t, h0 + 64, w[t].x.qt * 128, w[t].x.b);
-                            }
+            ListWalk<MODE> w(t);
+            ListGroup last;  // the previous tile's groups: its V goes one step after its K
+            int tiles = 0, unit = 0;
+            bool ok = true, more = w.next(p);
+            int ahead = more ? fetch(w.x, w.x.j0) : -1;  // entries of the next tile, loaded a step ahead
+            while (ok && more) {
+                const ListUnit x = w.x;
+                if (!wait(q_empty + t, (unit & 1) ^ 1)) break;
+                if (elect_one()) {
+                    uint8_t* dst = smem + SQ + t * Q_BYTES;
+                    const int h0 = x.h * 128;
+                    if (MODE == BLOCKS) {
+                        const int nj = p.g.nq(2), ni = p.g.nq(1);
+                        const int j = (x.qt % nj) * p.g.qb[2], i = (x.qt / nj % ni) * p.g.qb[1], f = (x.qt / nj / ni) * p.g.qb[0];
+                        mbar_expect_tx(q_full + t, p.rows * 256);
+                        tma_load_5d(dst, &tmQ, q_full + t, h0, j, i, f, x.b);
+                        tma_load_5d(dst + Q_HALF, &tmQ, q_full + t, h0 + 64, j, i, f, x.b);
+                    } else {
+                        mbar_expect_tx(q_full + t, Q_BYTES);
+                        tma_load_3d(dst, &tmQ, q_full + t, h0, x.qt * 128, x.b);
+                        tma_load_3d(dst + Q_HALF, &tmQ, q_full + t, h0 + 64, x.qt * 128, x.b);
+                    }
+                }
+                __syncwarp();
+                qpar = unit & 1;
+                ++unit;
+                for (int k = 0; ok && k <= x.n; ++k) {
+                    const ListGroup prev = last;
+                    if (k < x.n) {
+                        last = group_of(x, x.j0 + k, ahead);
+                        if (k + 1 < x.n) {
+                            ahead = fetch(x, x.j0 + k + 1);
+                        } else {
+                            more = w.next(p);
+                            if (more) ahead = fetch(w.x, w.x.j0);
                         }
-                        qpar[t] = unit[t] & 1;
-                        ++unit[t];
+                        write_mask(x, last, masks + t * MASKS + (tiles & (MASKS - 1)));
+                        ++tiles;
+                        ok = load(&tmK, x, last);
                     }
-                    const ListGroup prev = last[t];
-                    if (k < w[t].x.n) {
-                        last[t] = group_at(w[t].x, w[t].x.j0 + k);
-                        write_mask(w[t].x, last[t], masks + t * MASKS + (tiles[t] & (MASKS - 1)));
-                        ++tiles[t];
-                        ok = load(&tmK, w[t].x, last[t]);
-                    }
-                    if (ok && k > 0) ok = load(&tmV, w[t].x, prev);
-                    if (++w[t].k > w[t].x.n) w[t].next(p);
+                    if (ok && k > 0) ok = load(&tmV, x, prev);
                 }
             }
-        } else if (warp == 1) {
-            // ---------------- MMA issuer ----------------
-            // the whole warp runs the loop; lane 0 waits, one elected lane issues
-            constexpr uint32_t ID_QK = idesc_bf16(128, 128, false);
-            constexpr uint32_t ID_QK64 = idesc_bf16(128, 64, false);
+        } else {
+            // ---------------- MMA issuer of stream t ----------------
+            // the whole warp runs the loop; one elected lane issues
+            constexpr uint32_t ID_QK = idesc_bf16(128, KEYS, false);
             constexpr uint32_t ID_PV = idesc_bf16(128, 128, true);
-            const uint64_t dq = sdesc_kmajor_sw128(smem_u32(smem + SQ));
-            const uint64_t dk = sdesc_kmajor_sw128(smem_u32(smem + SKV));
-            const uint64_t dv = sdesc_mnmajor_sw128(smem_u32(smem + SKV), HALF_BYTES);
+            const uint64_t dq = sdesc_kmajor_sw128(smem_u32(smem + SQ + t * Q_BYTES));
+            const uint64_t dk = sdesc_kmajor_sw128(smem_u32(ring));
+            const uint64_t dv = sdesc_mnmajor_sw128(smem_u32(ring), KV_HALF);
+            const uint32_t ts = tmem + t * 128, to = tmem + 256 + t * 128;
             auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-                int r = 1;
-                if (lane == 0) r = mbar_spin(bar, parity, abort_flag, p.wc) ? 1 : 0;
-                return __shfl_sync(0xffffffffu, r, 0) != 0;
+                return warp_spin(bar, parity, abort_flag, p.wc);
             };
-            // S_t = Q_t K^T: all 128 keys, keys 64..127 (columns P does not
-            // occupy) or keys 0..63 (after the P.V that reads P there)
-            enum { S_ALL, S_HI, S_LO };
-            auto issue_s = [&](int t, int slot, bool last, int part) {
-                tc_fence_after();
-                const uint64_t a = dq + (uint64_t)((t * TILE_BYTES) >> 4);
-                const uint64_t b = dk + (uint64_t)((slot * TILE_BYTES + (part == S_HI ? 64 * 128 : 0)) >> 4);
-                const uint32_t d = tmem + t * 128 + (part == S_HI ? 64 : 0);
-                const uint32_t idesc = part == S_ALL ? ID_QK : ID_QK64;
-                if (elect_one()) {
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk) {
-                        const uint32_t o = ((kk >> 2) * HALF_BYTES + (kk & 3) * 32) >> 4;
-                        umma_bf16_ss(d, a + o, b + o, idesc, kk != 0);
-                    }
-                    if (part != S_HI) {
-                        umma_commit(s_full + t);
-                        umma_commit(kv_empty + slot);
-                        if (last) umma_commit(q_empty + t);
-                    }
-                }
-                __syncwarp();
-                issued = true;
-            };
-            // one K = 64 half of O_t += P_t V, P_t read from the S_t columns
-            auto issue_pv = [&](int t, int slot, bool first, bool last, int half) {
-                tc_fence_after();
-                const uint64_t b = dv + (uint64_t)((slot * TILE_BYTES) >> 4);
-                if (elect_one()) {
-#pragma unroll
-                    for (int kk = half * 4; kk < half * 4 + 4; ++kk)
-                        umma_bf16_ts(tmem + 256 + t * 128, tmem + t * 128 + kk * 8, b + ((kk * 2048) >> 4), ID_PV,
-                                     !(first && kk == 0));
-                    if (half == 1) {
-                        umma_commit(kv_empty + slot);
-                        if (last) umma_commit(o_final + t);
-                    }
-                }
-                __syncwarp();
-            };
-            ListWalk<MODE> w[2];
-            int c = 0, tiles[2] = {0, 0}, unit[2] = {0, 0};
+            ListWalk<MODE> w(t);
+            int c = 0, tiles = 0, unit = 0;
             bool ok = true;
-            for (int t = 0; t < 2; ++t) w[t].start(p, t);
-            while (ok && (w[0].live(p) || w[1].live(p))) {
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (!ok || !w[t].live(p)) continue;
-                    const int k = w[t].k, n = w[t].x.n;
-                    const int sk = c % SLOTS;  // slot of K(k)
-                    const bool more = k < n, last_s = k == n - 1;
-                    if (more) {
+            while (ok && w.next(p)) {
+                const int n = w.x.n;
+                if (!wait(q_full + t, unit & 1)) break;
+                ++unit;
+                for (int k = 0; k <= n; ++k) {
+                    const int at = tiles;  // tile k, counted over the stream's units
+                    if (k < n) {
+                        // S(k): its buffer held P(k - 2), whose P.V went out two steps ago
+                        const int slot = c % SLOTS;
                         const uint32_t phase = (c / SLOTS) & 1;
                         ++c;
-                        if (k == 0) {
-                            if (!wait(q_full + t, unit[t] & 1) || !wait(kv_full + sk, phase)) { ok = false; continue; }
-                            issue_s(t, sk, last_s, S_ALL);
-                            ++unit[t];
-                        } else {
-                            if (!wait(s_read + t, (tiles[t] - 1) & 1) || !wait(kv_full + sk, phase)) { ok = false; continue; }
-                            issue_s(t, sk, last_s, S_HI);
+                        if (!wait(full + slot, phase)) { ok = false; break; }
+                        tc_fence_after();
+                        const uint64_t b = dk + (uint64_t)((slot * SLOT_BYTES) >> 4);
+                        const uint32_t d = ts + (at & 1) * KEYS;
+                        if (elect_one()) {
+#pragma unroll
+                            for (int kk = 0; kk < 8; ++kk)
+                                umma_bf16_ss(d, dq + (((kk >> 2) * Q_HALF + (kk & 3) * 32) >> 4),
+                                             b + (((kk >> 2) * KV_HALF + (kk & 3) * 32) >> 4), ID_QK, kk != 0);
+                            umma_commit(s_full + 2 * t + (at & 1));
+                            umma_commit(empty + slot);
+                            if (k == n - 1) umma_commit(q_empty + t);
                         }
+                        __syncwarp();
+                        issued = true;
+                        ++tiles;
                     }
                     if (k > 0) {
-                        const int sv = c % SLOTS;
+                        // O += P(k - 1) V(k - 1)
+                        const int slot = c % SLOTS;
                         const uint32_t phase = (c / SLOTS) & 1;
                         ++c;
-                        const uint32_t tp = (tiles[t] - 1) & 1;  // phase of tile k - 1
-                        if (!wait(kv_full + sv, phase)) { ok = false; continue; }
-                        if (MODE == PAGES && k == n && w[t].x.dirty) {
+                        const int prev = at - 1;
+                        if (!wait(full + slot, phase)) { ok = false; break; }
+                        if (MODE == PAGES && k == n && w.x.dirty) {
                             // rows past the sequence hold foreign memory: 0 * NaN would reach O
-                            const int valid = w[t].x.length - (w[t].x.j0 + n - 1) * 128;  // 1..127
-                            const uint32_t base = smem_u32(smem + SKV + sv * TILE_BYTES);
-                            for (int i = valid * 8 + lane; i < 1024; i += 32) {
+                            const int valid = w.x.length - (w.x.j0 + n - 1) * KEYS;  // 1..63
+                            const uint32_t base = smem_u32(ring + slot * SLOT_BYTES);
+                            for (int i = valid * 8 + lane; i < KEYS * 8; i += 32) {
                                 st_shared_v4(base + i * 16, 0, 0, 0, 0);
-                                st_shared_v4(base + HALF_BYTES + i * 16, 0, 0, 0, 0);
+                                st_shared_v4(base + KV_HALF + i * 16, 0, 0, 0, 0);
                             }
                             fence_proxy_async_smem();
                             __syncwarp();
                         }
-                        if (!wait(p_part + t, tp)) { ok = false; continue; }
-                        issue_pv(t, sv, k == 1, false, 0);
-                        if (!wait(p_full + t, tp)) { ok = false; continue; }
-                        issue_pv(t, sv, false, k == n, 1);
-                        if (more) issue_s(t, sk, last_s, S_LO);
+                        if (!wait(p_full + 2 * t + (prev & 1), (prev >> 1) & 1)) { ok = false; break; }
+                        tc_fence_after();
+                        const uint64_t b = dv + (uint64_t)((slot * SLOT_BYTES) >> 4);
+                        if (elect_one()) {
+#pragma unroll
+                            for (int kk = 0; kk < KEYS / 16; ++kk)
+                                umma_bf16_ts(to, ts + (prev & 1) * KEYS + kk * 8, b + ((kk * 2048) >> 4), ID_PV,
+                                             !(k == 1 && kk == 0));
+                            umma_commit(empty + slot);
+                            umma_commit(pv_done + 2 * t + (prev & 1));
+                        }
+                        __syncwarp();
                     }
-                    if (more) ++tiles[t];
-                    if (++w[t].k > n) w[t].next(p);
                 }
             }
         }
@@ -439,78 +479,66 @@ __global__ void __launch_bounds__(alist::THREADS, 1)
         const int qq = warp & 3;                         // TMEM lane quarter
         const int r = qq * 32 + lane;                    // row inside the tile == TMEM lane
         const uint32_t lane_off = static_cast<uint32_t>(qq * 32) << 16;
-        const uint32_t TS = tmem + t * 128 + lane_off;   // S_t (and P_t)
+        const uint32_t TS0 = tmem + t * 128 + lane_off;  // the S (and P) buffers
         const uint32_t TO = tmem + 256 + t * 128 + lane_off;
-        const int Lq = MODE == BLOCKS ? p.g.q_tokens() : p.T;
         bool ok = true;
-        int g = 0, iu = 0;  // tiles and non-empty units so far
+        int g = 0;  // tiles so far
         for (int u = blockIdx.x * 2 + t; ok && u < p.units; u += 2 * gridDim.x) {
-            const ListUnit x = list_unit<MODE>(p, u);
-            // query token of this thread's row, -1 for none
-            int token = -1;
-            if (MODE == BLOCKS) {
-                const int nj = p.g.nq(2), ni = p.g.nq(1);
-                const int f = (x.qt / nj / ni) * p.g.qb[0] + r / (p.g.qb[2] * p.g.qb[1]);
-                const int i = (x.qt / nj % ni) * p.g.qb[1] + r / p.g.qb[2] % p.g.qb[1];
-                const int j = (x.qt % nj) * p.g.qb[2] + r % p.g.qb[2];
-                if (r < p.rows && f < p.g.q[0] && i < p.g.q[1] && j < p.g.q[2]) token = (f * p.g.q[1] + i) * p.g.q[2] + j;
-            } else if (x.qt * 128 + r < p.T) {
-                token = x.qt * 128 + r;
+            // only what the tile loop needs stays in registers beside S
+            int n;
+            bool active;
+            {
+                const ListUnit x = list_unit<MODE>(p, u);
+                n = x.n;
+                active = __any_sync(0xffffffffu, list_token<MODE>(p, x.qt, r) >= 0);
             }
-            const bool active = __any_sync(0xffffffffu, token >= 0);
             float m_run = -INFINITY, l_run = 0.0f;
-            for (int j = 0; j < x.n; ++j, ++g) {
+            for (int j = 0; j < n; ++j, ++g) {
+                const int buf = g & 1;
+                const uint32_t TS = TS0 + buf * KEYS;
                 // all tcgen05.ld/st below are warp-collective: the warp's decisions stay uniform
-                if (!__all_sync(0xffffffffu, mbar_wait(s_full + t, g & 1, abort_flag, p.wc))) { ok = false; break; }
+                if (!__all_sync(0xffffffffu, mbar_wait(s_full + 2 * t + buf, (g >> 1) & 1, abort_flag, p.wc))) { ok = false; break; }
                 tc_fence_after();
                 if (!active) {  // no row here: the S columns stay as they are, nothing reads their product
                     __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(s_read + t);
-                        mbar_arrive(p_part + t);
-                        mbar_arrive(p_full + t);
-                    }
+                    if (lane == 0) mbar_arrive(p_full + 2 * t + buf);
                     continue;
                 }
-                uint32_t sv[4][32];
+                uint32_t sv[2][32];
+                tmem_ld32(TS, sv[0]);
+                tmem_ld32(TS + 32, sv[1]);
+                const uint2 mk = masks[t * MASKS + (g & (MASKS - 1))];
+                tmem_ld_wait(sv[0]);
+                tmem_ld_wait(sv[1]);
+                if ((mk.x & mk.y) != 0xffffffffu) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(TS + c * 32, sv[c]);
-                const uint4 mk = masks[t * MASKS + (g & (MASKS - 1))];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld_wait(sv[c]);
-                {  // S_t is in registers: the MMA may rewrite its upper key half
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(s_read + t);
-                }
-                const uint32_t mw[4] = {mk.x, mk.y, mk.z, mk.w};
-                if ((mw[0] & mw[1] & mw[2] & mw[3]) != 0xffffffffu) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                    for (int c = 0; c < 2; ++c) {
+                        const uint32_t w = c ? mk.y : mk.x;
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (!(mw[c] >> i & 1)) sv[c][i] = __float_as_uint(-INFINITY);
+                            if (!(w >> i & 1)) sv[c][i] = __float_as_uint(-INFINITY);
+                    }
                 }
-                // row maximum: eight independent 3-input max chains
-                float mx[8];
+                // row maximum: four independent 3-input max chains
+                float mx[4];
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
+                for (int q = 0; q < 4; ++q) {
                     const uint32_t* v = &sv[q >> 1][(q & 1) * 16];
                     float a = fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1]));
 #pragma unroll
                     for (int i = 2; i < 16; i += 2) a = max3f(a, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
                     mx[q] = a;
                 }
-                const float m_tile =
-                    max3f(max3f(mx[0], mx[1], mx[2]), max3f(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * p.scale_log2;
+                const float m_tile = fmaxf(max3f(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
                 const float m_new = fmaxf(m_run, m_tile);
                 const bool rescale = m_new > m_run + RESCALE_THRESHOLD;
                 const float m_use = rescale ? m_new : m_run;
                 const float m_sub = m_use == -INFINITY ? 0.0f : m_use;  // every key so far masked: all exponentials are 0
-                // O_t is idle here (the commit of S_t also covered the previous P_t V) and
-                // must be rescaled before the first half of this tile's P_t V is issued
                 const float alpha = rescale ? ex2_approx(m_run - m_use) : 1.0f;  // 0 on the first tile
                 if (j > 0 && __any_sync(0xffffffffu, rescale)) {
+                    // O_t is scaled between the P.V of the previous tile and this tile's
+                    if (!__all_sync(0xffffffffu, mbar_wait(pv_done + 2 * t + ((g - 1) & 1), ((g - 1) >> 1) & 1, abort_flag, p.wc))) { ok = false; break; }
+                    tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
                         uint32_t ov[32];
@@ -522,12 +550,12 @@ __global__ void __launch_bounds__(alist::THREADS, 1)
                     }
                 }
                 // probabilities on packed fp32 pairs, summed in fp32 and rounded to bf16 (the
-                // tensor core's operand type: half a step is 2^-9 of each) over their S columns
+                // tensor core's operand type: half a step is 2^-8 of each) over their S columns
                 uint64_t ps2[2] = {0ull, 0ull};
                 const uint64_t scale2 = f2pack(p.scale_log2, p.scale_log2);
                 const uint64_t negm2 = f2pack(-m_sub, -m_sub);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < 2; ++c) {
                     uint32_t pc[16];
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) {
@@ -539,12 +567,6 @@ __global__ void __launch_bounds__(alist::THREADS, 1)
                         pc[i / 2] = pack_bf16(e0, e1);
                     }
                     tmem_st16(TS + c * 16, pc);
-                    if (c == 1) {  // keys 0..63 (and any O rescale) stored: their P.V may start
-                        tmem_st_wait();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(p_part + t);
-                    }
                 }
                 float ps[4];
                 f2unpack(ps2[0], ps[0], ps[1]);
@@ -557,13 +579,12 @@ __global__ void __launch_bounds__(alist::THREADS, 1)
                 l_run += (ps[0] + ps[1]) + (ps[2] + ps[3]);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_full + t);
+                if (lane == 0) mbar_arrive(p_full + 2 * t + buf);
             }
             if (!ok) break;
             // the unit's output: O_t / l once its last P.V has landed (zero rows where no key was left)
-            if (x.n > 0) {
-                if (!__all_sync(0xffffffffu, mbar_wait(o_final + t, iu & 1, abort_flag, p.wc))) { ok = false; break; }
-                ++iu;
+            if (n > 0) {
+                if (!__all_sync(0xffffffffu, mbar_wait(pv_done + 2 * t + ((g - 1) & 1), ((g - 1) >> 1) & 1, abort_flag, p.wc))) { ok = false; break; }
                 tc_fence_after();
             }
             if (!active) continue;
@@ -571,26 +592,33 @@ __global__ void __launch_bounds__(alist::THREADS, 1)
             const float inv = none ? 0.0f : 1.0f / l_run;
             const float lse2 = none ? -INFINITY : m_run + log2f(l_run);
             const bool direct = p.splits == 1;
+            // the unit's place worked out again, not carried through the loop: S leaves no registers for it
+            int again = u, row = r;
+            asm volatile("" : "+r"(again), "+r"(row));
+            const int per = p.nqb * p.heads * p.B, at = again % per;
+            const int qt = at % p.nqb, h = at / p.nqb % p.heads, b = at / p.nqb / p.heads;
+            const int token = list_token<MODE>(p, qt, row);
+            const int Lq = MODE == BLOCKS ? p.g.q_tokens() : p.T;
             if (token >= 0) {
                 if (!direct)
                     p.part_lse[(long long)u * p.rows + r] = lse2;
                 else if (p.lse)
-                    p.lse[((long long)x.b * p.heads + x.h) * Lq + token] = lse2 * 0.6931471805599453f;
+                    p.lse[((long long)b * p.heads + h) * Lq + token] = lse2 * 0.6931471805599453f;
             }
-            if (!direct && x.n == 0) continue;  // the join does not read rows whose sum is empty
-            __nv_bfloat16* orow = p.o + ((long long)x.b * Lq + token) * p.ldo + x.h * 128;
+            __nv_bfloat16* orow = p.o + ((long long)b * Lq + token) * p.ldo + h * 128;
+            if (n == 0) {  // a list without keys; the join does not read rows whose sum is empty
+                if (direct && token >= 0)
+                    for (int c = 0; c < 16; ++c) reinterpret_cast<uint4*>(orow)[c] = make_uint4(0, 0, 0, 0);
+                continue;
+            }
             float* prow = p.part_o + ((long long)u * p.rows + r) * 128;
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
                 uint32_t ov[32];
-                if (x.n > 0) {
-                    tmem_ld32(TO + c * 32, ov);
-                    tmem_ld_wait(ov);
-                }
-                if (none) {
+                tmem_ld32(TO + c * 32, ov);
+                tmem_ld_wait(ov);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) ov[i] = 0;
-                }
+                for (int i = 0; i < 32; ++i) ov[i] = none ? 0u : ov[i];
                 if (token >= 0 && direct) {
                     uint4* dst = reinterpret_cast<uint4*>(orow + c * 32);
 #pragma unroll
@@ -615,18 +643,21 @@ __global__ void __launch_bounds__(alist::THREADS, 1)
     if (*abort_flag) {
         // a wait gave up somewhere in the CTA: let this CTA's own loads and MMAs
         // land (bounded) before its shared and tensor memory are released
-        if (warp == 0 && lane == 0) {
-            for (int t = 0; t < 2; ++t)
-                if (qpar[t] >= 0) mbar_drain(q_full + t, static_cast<uint32_t>(qpar[t]), 200000000ull);
-            for (int s = 0; s < SLOTS; ++s)
-                if (armed & (1u << s)) mbar_drain(kv_full + s, (par >> s) & 1, 200000000ull);
-        } else if (warp == 1 && issued) {
+        if (warp == 0 || warp == 2) {
+            const int t = warp >> 1;
+            if (lane == 0) {
+                if (qpar >= 0) mbar_drain(q_full + t, static_cast<uint32_t>(qpar), 200000000ull);
+                for (int s = 0; s < SLOTS; ++s)
+                    if (armed & (1u << s)) mbar_drain(kv_full + t * SLOTS + s, (par >> s) & 1, 200000000ull);
+            }
+        } else if ((warp == 1 || warp == 3) && issued) {
             if (elect_one()) {  // the lane that issued the MMAs
-                umma_commit(drain);
-                mbar_drain(drain, 0, 200000000ull);
+                umma_commit(drain + (warp >> 1));
+                mbar_drain(drain + (warp >> 1), 0, 200000000ull);
             }
             __syncwarp();
         }
+        __syncthreads();
     }
     if (warp == 1) {
         __syncwarp();
@@ -748,6 +779,19 @@ int log2_of(int v) {
     return n;
 }
 
+FastDiv fast_div(int d) {
+    const uint32_t shift = (uint32_t)log2_of(d);
+    const uint64_t mul = ((1ull << 32) * ((1ull << shift) - (uint64_t)d)) / (uint64_t)d + 1;
+    return FastDiv{(uint32_t)mul, shift};
+}
+
+// Token groups of a block or page of `tokens` (16, 32, 64 or 128) tokens.
+void list_groups(int tokens, ListParams* p) {
+    p->log_sub = tokens > alist::KEYS ? 1 : 0;
+    p->log_group = log2_of(tokens) - p->log_sub;
+    p->E = alist::KEYS >> p->log_group;
+}
+
 bool blocks_plan(int B, int heads, const BlockGrid& g, int topk, ListParams* p) {
     p->B = B;
     p->heads = heads;
@@ -756,10 +800,23 @@ bool blocks_plan(int B, int heads, const BlockGrid& g, int topk, ListParams* p) 
     p->nkb = g.k_blocks();
     p->rows = g.q_volume();
     p->topk = topk;
-    p->log_group = log2_of(g.k_volume());
-    p->E = 128 >> p->log_group;
+    list_groups(g.k_volume(), p);
+    for (int a = 0; a < 3; ++a) {
+        p->sub[a] = g.kb[a];
+        p->step[a] = 0;
+    }
+    p->nk1 = g.nk(1);
+    p->nk2 = g.nk(2);
+    p->by_nk1 = fast_div(p->nk1);
+    p->by_nk2 = fast_div(p->nk2);
+    if (p->log_sub) {  // two groups of 64: halves of the block's longest axis (a power of two, as its volume is)
+        int a = 0;
+        for (int i = 1; i < 3; ++i)
+            if (g.kb[i] > g.kb[a]) a = i;
+        p->sub[a] = p->step[a] = g.kb[a] / 2;
+    }
     const long long per = (long long)p->nqb * heads * B;
-    p->splits = list_splits(per, (topk + p->E - 1) / p->E, p->rows);
+    p->splits = list_splits(per, ((topk << p->log_sub) + p->E - 1) / p->E, p->rows);
     return per * p->splits < (1ll << 31) - 1024;
 }
 
@@ -770,10 +827,9 @@ bool pages_plan(int B, int heads, int T, int max_pages, int page_size, ListParam
     p->nqb = (T + 127) / 128;
     p->rows = T < 128 ? T : 128;
     p->max_pages = max_pages;
-    p->log_group = log2_of(page_size);
-    p->E = 128 >> p->log_group;
+    list_groups(page_size, p);
     const long long per = (long long)p->nqb * heads * B;
-    p->splits = list_splits(per, (max_pages + p->E - 1) / p->E, p->rows);
+    p->splits = list_splits(per, ((max_pages << p->log_sub) + p->E - 1) / p->E, p->rows);
     return per * p->splits < (1ll << 31) - 1024;
 }
 
@@ -809,7 +865,7 @@ cudaError_t launch_attention_blocks(const void* q, long long ldq, const void* k,
         return make_tmap_5d(m, ptr, dims, strides, 64, box[2], box[1], box[0]);
     };
     CUtensorMap tq, tk, tv;
-    if (!map(&tq, q, ldq, g.q, g.qb) || !map(&tk, k, ldk, g.k, g.kb) || !map(&tv, v, ldv, g.k, g.kb))
+    if (!map(&tq, q, ldq, g.q, g.qb) || !map(&tk, k, ldk, g.k, p.sub) || !map(&tv, v, ldv, g.k, p.sub))
         return cudaErrorInvalidValue;
     return launch_list<alist::BLOCKS>(tq, tk, tv, p, ws, ctx);
 }
@@ -826,10 +882,11 @@ cudaError_t launch_attention_paged(const void* q, long long ldq, const KvPages& 
     p.ldo = ldo;
     p.lse = lse;
     const uint64_t width = (uint64_t)heads * 128;
+    const uint32_t group = 1u << p.log_group;
     CUtensorMap tq, tk, tv;
     if (!make_tmap_3d(&tq, q, width, T, B, ldq, (uint64_t)ldq * T, 64, 128) ||
-        !make_tmap_3d(&tk, c.k, width, c.page_size, c.num_pages, c.token_stride, c.page_stride, 64, c.page_size) ||
-        !make_tmap_3d(&tv, c.v, width, c.page_size, c.num_pages, c.token_stride, c.page_stride, 64, c.page_size))
+        !make_tmap_3d(&tk, c.k, width, c.page_size, c.num_pages, c.token_stride, c.page_stride, 64, group) ||
+        !make_tmap_3d(&tv, c.v, width, c.page_size, c.num_pages, c.token_stride, c.page_stride, 64, group))
         return cudaErrorInvalidValue;
     return launch_list<alist::PAGES>(tq, tk, tv, p, ws, ctx);
 }
