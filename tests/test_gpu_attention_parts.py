@@ -522,3 +522,61 @@ def test_zero_wait_limit_reports_and_recovers(mode):
     again = run()
     B().op_sync()
     assert torch.equal(clean, again)
+
+
+@pytest.mark.parametrize("lens", [[0] * 7, [0, 0, 9000, 0, 1, 0, 0], [4000, 0, 64, 128, 1, 63, 3000], [64] * 7, [1] * 7,
+                                  [100, 5000, 2000, 7000, 3, 0, 0]])
+@pytest.mark.parametrize("T", [1, 140])
+def test_attention_paged_ranges_cut_sequences_of_all_lengths(lens, T):
+    """The tiles of all sequences are cut into even ranges: empty sequences at either end, sequences that a range
+    holds whole, that several share, that end on a range's border."""
+    heads, page, per = 3, 16, 563
+    kc, vc, table = cache(len(lens), per, page, heads, 101)
+    q = rnd((len(lens), T, heads * 128), 102)
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    lse = torch.full((len(lens), heads, T), math.nan, device="cuda")
+    out = torch.full_like(q, math.nan)
+    B().op_attention_paged(q, kc, vc, table, ln, heads, out=out, lse=lse)
+    B().op_sync()
+    check(out, lse, *R.attention_paged(q, kc, vc, table, ln, heads))
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e-18, 1e18, 1e30])
+def test_block_select_at_the_ends_of_the_range(scale):
+    """Products that underflow or overflow 32 bits are still ranked by their 64-bit scores."""
+    heads, args = 2, ((1, 1, 256), (1, 1, 80 * 16), (1, 1, 64), (1, 1, 16))
+    q, k = rnd((1, 256, 256), 111, scale), rnd((1, 1280, 256), 112, scale)
+    blocks, counts = B().op_block_select(q, k, heads, *args, 9)
+    B().op_sync()
+    want = R.select(q, k, heads, *args, 9)
+    assert torch.equal(blocks.cpu(), want[0]) and torch.equal(counts.cpu(), want[1])
+
+
+def test_block_select_close_scores_are_ranked_by_their_last_bits():
+    """Key blocks that differ by one bf16 step in one element of one token: far below 32-bit rounding of the
+    score's sum, and more of them than one warp holds at a time."""
+    nk = 300
+    base = rnd((1, 16, 128), 113)
+    k = base.repeat(nk, 1, 1)
+    order = torch.randperm(nk, generator=torch.Generator().manual_seed(114))
+    for n in range(nk):
+        i = int(order[n])
+        k[n, i // 128, i % 128] *= 1 + 2.0 ** -7
+    k = k.reshape(1, nk * 16, 128).contiguous()
+    q = rnd((1, 128, 128), 115)
+    for topk in (3, 20, 150):
+        args = (1, (1, 1, 128), (1, 1, nk * 16), (1, 1, 32), (1, 1, 16), topk)
+        blocks, counts = B().op_block_select(q, k, *args)
+        B().op_sync()
+        want = R.select(q, k, *args)
+        assert torch.equal(blocks.cpu(), want[0]) and torch.equal(counts.cpu(), want[1])
+
+
+@pytest.mark.parametrize("nk", [2048, 2049])
+def test_block_select_on_both_sides_of_the_two_stage_limit(nk):
+    args = (2, (1, 1, 100), (1, 1, nk * 16), (1, 1, 32), (1, 1, 16), 77)
+    q, k = rnd((1, 100, 256), 116), rnd((1, nk * 16, 256), 117)
+    blocks, counts = B().op_block_select(q, k, *args)
+    B().op_sync()
+    want = R.select(q, k, *args)
+    assert torch.equal(blocks.cpu(), want[0]) and torch.equal(counts.cpu(), want[1])

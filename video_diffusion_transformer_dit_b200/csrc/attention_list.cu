@@ -34,9 +34,14 @@
 //          V rows of a tile past the sequence's end inside a page before its P.V;
 //   4..11  softmax of stream 0 / 1, one query row per thread; warps without a
 //          row only keep the barriers' counts.
-// Where there are too few query tiles to fill the GPU, lists are split: each
-// split writes its normalised fp32 rows and their log-sum-exp, and
-// list_join_kernel joins them.
+// Where there are too few query tiles to fill the GPU, lists are split.  Blocks:
+// each list into `splits` parts.  Pages: sequences differ in length, so the tiles
+// of all sequences, one after the other, are cut into `splits` even ranges, and a
+// unit is one range for one head and query tile; it may hold the end of one
+// sequence, whole ones and the beginning of another.  A part of a list writes its
+// normalised fp32 rows and their log-sum-exp, and list_join_kernel joins them.
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -54,7 +59,9 @@ constexpr int SQ = 0;
 constexpr int SKV = SQ + 2 * Q_BYTES;
 constexpr int SMASK = SKV + 2 * SLOTS * SLOT_BYTES;
 constexpr int SBAR = SMASK + 2 * MASKS * 8;
-constexpr int SMEM_BYTES = SBAR + 320 + 1024;
+constexpr int SSTART = SBAR + 320;         // pages: first tile of each sequence
+constexpr int MAX_SEQS = 256;              // sequences per launch (pages)
+constexpr int SMEM_BYTES = SSTART + (MAX_SEQS + 1) * 4 + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
 constexpr int THREADS = 384;
 constexpr int REGS_LAUNCH = 168;
@@ -102,52 +109,94 @@ struct ListParams {
     WaitCtl wc;
 };
 
-// One unit: its head, sample, query tile and the tiles [j0, j0 + n) of its list.
+// One list or part of one: its head, sample, query tile and tiles [j0, j0 + n).
 struct ListUnit {
     int b, h, qt, j0, n;
     int length;             // groups in the list (blocks) or tokens in the cache (pages)
+    long long part;         // place of its partial rows, -1: the whole list, written to the output
     bool dirty;             // pages: the last tile ends inside a page
 };
 
-template <alist::Mode MODE>
-__device__ __forceinline__ ListUnit list_unit(const ListParams& p, int u) {
-    ListUnit x;
-    // splits slowest: CTAs that run together read the same tokens of several heads
-    const int per = p.nqb * p.heads * p.B;
-    const int s = u / per;
-    int r = u - s * per;
-    x.qt = r % p.nqb;
-    r /= p.nqb;
-    x.h = r % p.heads;
-    x.b = r / p.heads;
-    int tiles;
-    if (MODE == alist::BLOCKS) {
-        const int c = __ldg(p.counts + ((long long)x.b * p.heads + x.h) * p.nqb + x.qt);
-        x.length = min(max(c, 0), p.topk) << p.log_sub;
-        tiles = (x.length + p.E - 1) / p.E;
-    } else {
-        const int cap = p.max_pages << (p.log_group + p.log_sub);
-        x.length = min(max(__ldg(p.lens + x.b), 0), cap);
-        tiles = (x.length + alist::KEYS - 1) / alist::KEYS;
-    }
-    x.j0 = (int)((long long)tiles * s / p.splits);
-    const int j1 = (int)((long long)tiles * (s + 1) / p.splits);
-    x.n = j1 - x.j0;
-    x.dirty = MODE == alist::PAGES && j1 == tiles && (x.length & ((1 << p.log_group) - 1)) != 0;
-    return x;
+// Tiles of sequence b of a paged cache, and its tokens.
+__device__ __forceinline__ int page_tokens(const ListParams& p, int b) {
+    return min(max(__ldg(p.lens + b), 0), p.max_pages << (p.log_group + p.log_sub));
+}
+__device__ __forceinline__ uint32_t page_tiles(int tokens) { return ((uint32_t)tokens + alist::KEYS - 1) / alist::KEYS; }
+
+// Ranges in use: none without a tile (but for the one that all empty sequences fall to).
+__device__ __forceinline__ uint32_t page_ranges(const ListParams& p, uint32_t total) {
+    return min((uint32_t)p.splits, max(total, 1u));
 }
 
-// Units of one stream that have tiles: next() takes the next one (false: none left).
+// What one stream works through: next() takes the next list (false: none left).
+// A list without keys comes with n = 0 (blocks also an empty part of a list).
 template <alist::Mode MODE>
 struct ListWalk {
     ListUnit x;
-    int u;
-    __device__ __forceinline__ explicit ListWalk(int t) : u(blockIdx.x * 2 + t - 2 * gridDim.x) {}
+    int u, b;                  // unit; pages: next sequence of the range
+    uint32_t lo, hi;           // pages: the unit's range of tiles
+    const uint32_t* start;     // pages: first tile of each sequence, [B + 1]
+    __device__ __forceinline__ ListWalk(int t, const uint32_t* starts)
+        : u(blockIdx.x * 2 + t - 2 * gridDim.x), b(0x7fffffff), lo(0), hi(0), start(starts) {}
+
     __device__ __forceinline__ bool next(const ListParams& p) {
-        do {
+        if constexpr (MODE == alist::BLOCKS) {
             u += 2 * gridDim.x;
             if (u >= p.units) return false;
-            x = list_unit<MODE>(p, u);
+            // splits slowest: CTAs that run together read the same tokens of several heads
+            const int per = p.nqb * p.heads * p.B;
+            const int s = u / per;
+            int r = u - s * per;
+            x.qt = r % p.nqb;
+            r /= p.nqb;
+            x.h = r % p.heads;
+            x.b = r / p.heads;
+            const int c = __ldg(p.counts + ((long long)x.b * p.heads + x.h) * p.nqb + x.qt);
+            x.length = min(max(c, 0), p.topk) << p.log_sub;
+            const int tiles = (x.length + p.E - 1) / p.E;
+            x.j0 = (int)((long long)tiles * s / p.splits);
+            x.n = (int)((long long)tiles * (s + 1) / p.splits) - x.j0;
+            x.part = p.splits > 1 ? u : -1;
+            x.dirty = false;
+            return true;
+        } else while (true) {
+            if (b < p.B && (start[b] < hi || (start[b] == hi && hi == start[p.B]))) {
+                const uint32_t first = start[b], end = start[b + 1];
+                x.b = b++;
+                const uint32_t s0 = max(first, lo), s1 = min(end, hi);
+                if (end > first && s1 <= s0) continue;
+                x.length = page_tokens(p, x.b);
+                x.j0 = (int)(s0 - first);
+                x.n = end > first ? (int)(s1 - s0) : 0;
+                x.part = end > first && (s0 != first || s1 != end) ? u * 2ll + (s0 > lo) : -1;
+                x.dirty = s1 == end && (x.length & ((1 << p.log_group) - 1)) != 0;
+                return true;
+            }
+            u += 2 * gridDim.x;
+            if (u >= p.units) return false;
+            const int inner = p.nqb * p.heads;
+            const uint32_t r = (uint32_t)(u / inner);
+            const int i = u - (int)r * inner;
+            x.qt = i % p.nqb;
+            x.h = i / p.nqb;
+            const uint32_t total = start[p.B], ranges = page_ranges(p, total);
+            b = p.B;
+            if (r >= ranges) continue;
+            lo = (uint32_t)((unsigned long long)total * r / ranges);
+            hi = (uint32_t)((unsigned long long)total * (r + 1) / ranges);
+            int b0 = 0, b1 = p.B;  // first sequence with tiles at or past lo (or none, at lo)
+            while (b0 < b1) {
+                const int m = (b0 + b1) >> 1;
+                if (start[m + 1] > lo || start[m] >= lo) b1 = m;
+                else b0 = m + 1;
+            }
+            b = b0;
+        }
+    }
+    // the next list that has tiles
+    __device__ __forceinline__ bool next_tiles(const ListParams& p) {
+        do {
+            if (!next(p)) return false;
             // read by every lane alike, but known to the compiler as warp-uniform only from
             // a broadcast: ring slots and descriptors that follow from it stay in uniform registers
             x.n = __shfl_sync(0xffffffffu, x.n, 0);
@@ -212,6 +261,7 @@ __global__ void __launch_bounds__(alist::THREADS, 1)
     uint64_t* drain = pv_done + 4;           // [2]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    uint32_t* starts = reinterpret_cast<uint32_t*>(smem + SSTART);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -241,6 +291,20 @@ __global__ void __launch_bounds__(alist::THREADS, 1)
     if (warp == 1) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
+    }
+    if (MODE == PAGES && warp == 2) {
+        uint32_t before = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            uint32_t n = b0 + lane < p.B ? page_tiles(page_tokens(p, b0 + lane)) : 0u;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t m = __shfl_up_sync(0xffffffffu, n, o);
+                if (lane >= o) n += m;
+            }
+            if (b0 + lane < p.B) starts[b0 + lane + 1] = before + n;
+            before += __shfl_sync(0xffffffffu, n, 31);
+        }
+        if (lane == 0) starts[0] = 0;
     }
     tc_fence_before();
     __syncthreads();
@@ -323,6 +387,34 @@ __global__ void __launch_bounds__(alist::THREADS, 1)
                 }
                 if (lane == 0) *dst = make_uint2(w[0], w[1]);
             };
+            // the tile's groups into a slot: coordinates broadcast, one lane issues all copies from
+            // uniform registers (a copy per lane is issued lane by lane, three times as slow)
+            auto gather = [&](auto groups, const CUtensorMap* tm, uint8_t* dst, uint64_t* bar, int h0, const ListGroup& o) {
+                constexpr int E = decltype(groups)::value;
+                int f[E], i[E], j[E], b[E];
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    i[e] = __shfl_sync(0xffffffffu, o.i, e);
+                    b[e] = __shfl_sync(0xffffffffu, o.b, e);
+                    if (MODE == BLOCKS) {
+                        f[e] = __shfl_sync(0xffffffffu, o.f, e);
+                        j[e] = __shfl_sync(0xffffffffu, o.j, e);
+                    }
+                }
+                if (elect_one()) {
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            uint8_t* to = dst + half * KV_HALF + e * (KEYS / E) * 128;
+                            if (MODE == BLOCKS)
+                                tma_load_5d(to, tm, bar, h0 + half * 64, j[e], i[e], f[e], b[e]);
+                            else
+                                tma_load_3d(to, tm, bar, h0 + half * 64, i[e], b[e]);
+                        }
+                }
+                __syncwarp();
+            };
             int c = 0;  // loads so far
             auto load = [&](const CUtensorMap* tm, const ListUnit& x, const ListGroup& o) -> bool {
                 const int slot = c % SLOTS;
@@ -331,31 +423,21 @@ __global__ void __launch_bounds__(alist::THREADS, 1)
                 if (!wait(empty + slot, phase ^ 1)) return false;
                 if (elect_one()) mbar_expect_tx(full + slot, SLOT_BYTES);
                 __syncwarp();
-                const int h0 = x.h * 128;
-                for (int e = 0; e < p.E; ++e) {  // coordinates broadcast: one lane issues from uniform registers
-                    uint8_t* dst = ring + slot * SLOT_BYTES + (e << p.log_group) * 128;
-                    const int f = __shfl_sync(0xffffffffu, o.f, e), i = __shfl_sync(0xffffffffu, o.i, e);
-                    const int b = __shfl_sync(0xffffffffu, o.b, e);
-                    if (MODE == BLOCKS) {
-                        const int j = __shfl_sync(0xffffffffu, o.j, e);
-                        if (elect_one()) {
-                            tma_load_5d(dst, tm, full + slot, h0, j, i, f, b);
-                            tma_load_5d(dst + KV_HALF, tm, full + slot, h0 + 64, j, i, f, b);
-                        }
-                    } else if (elect_one()) {
-                        tma_load_3d(dst, tm, full + slot, h0, i, b);
-                        tma_load_3d(dst + KV_HALF, tm, full + slot, h0 + 64, i, b);
-                    }
-                    __syncwarp();
-                }
+                uint8_t* dst = ring + slot * SLOT_BYTES;
+                if (p.E == 1)
+                    gather(std::integral_constant<int, 1>{}, tm, dst, full + slot, x.h * 128, o);
+                else if (p.E == 2)
+                    gather(std::integral_constant<int, 2>{}, tm, dst, full + slot, x.h * 128, o);
+                else
+                    gather(std::integral_constant<int, 4>{}, tm, dst, full + slot, x.h * 128, o);
                 armed |= 1u << slot;
                 par = (par & ~(1u << slot)) | phase << slot;
                 return true;
             };
-            ListWalk<MODE> w(t);
+            ListWalk<MODE> w(t, starts);
             ListGroup last;  // the previous tile's groups: its V goes one step after its K
             int tiles = 0, unit = 0;
-            bool ok = true, more = w.next(p);
+            bool ok = true, more = w.next_tiles(p);
             int ahead = more ? fetch(w.x, w.x.j0) : -1;  // entries of the next tile, loaded a step ahead
             while (ok && more) {
                 const ListUnit x = w.x;
@@ -385,7 +467,7 @@ __global__ void __launch_bounds__(alist::THREADS, 1)
                         if (k + 1 < x.n) {
                             ahead = fetch(x, x.j0 + k + 1);
                         } else {
-                            more = w.next(p);
+                            more = w.next_tiles(p);
                             if (more) ahead = fetch(w.x, w.x.j0);
                         }
                         write_mask(x, last, masks + t * MASKS + (tiles & (MASKS - 1)));
@@ -407,10 +489,10 @@ __global__ void __launch_bounds__(alist::THREADS, 1)
             auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
                 return warp_spin(bar, parity, abort_flag, p.wc);
             };
-            ListWalk<MODE> w(t);
+            ListWalk<MODE> w(t, starts);
             int c = 0, tiles = 0, unit = 0;
             bool ok = true;
-            while (ok && w.next(p)) {
+            while (ok && w.next_tiles(p)) {
                 const int n = w.x.n;
                 if (!wait(q_full + t, unit & 1)) break;
                 ++unit;
@@ -483,15 +565,11 @@ __global__ void __launch_bounds__(alist::THREADS, 1)
         const uint32_t TO = tmem + 256 + t * 128 + lane_off;
         bool ok = true;
         int g = 0;  // tiles so far
-        for (int u = blockIdx.x * 2 + t; ok && u < p.units; u += 2 * gridDim.x) {
-            // only what the tile loop needs stays in registers beside S
-            int n;
-            bool active;
-            {
-                const ListUnit x = list_unit<MODE>(p, u);
-                n = x.n;
-                active = __any_sync(0xffffffffu, list_token<MODE>(p, x.qt, r) >= 0);
-            }
+        ListWalk<MODE> w(t, starts);
+        while (w.next(p)) {
+            const int n = w.x.n;
+            const int token = list_token<MODE>(p, w.x.qt, r);
+            const bool active = __any_sync(0xffffffffu, token >= 0);
             float m_run = -INFINITY, l_run = 0.0f;
             for (int j = 0; j < n; ++j, ++g) {
                 const int buf = g & 1;
@@ -591,27 +669,21 @@ __global__ void __launch_bounds__(alist::THREADS, 1)
             const bool none = l_run == 0.0f;
             const float inv = none ? 0.0f : 1.0f / l_run;
             const float lse2 = none ? -INFINITY : m_run + log2f(l_run);
-            const bool direct = p.splits == 1;
-            // the unit's place worked out again, not carried through the loop: S leaves no registers for it
-            int again = u, row = r;
-            asm volatile("" : "+r"(again), "+r"(row));
-            const int per = p.nqb * p.heads * p.B, at = again % per;
-            const int qt = at % p.nqb, h = at / p.nqb % p.heads, b = at / p.nqb / p.heads;
-            const int token = list_token<MODE>(p, qt, row);
+            const bool direct = w.x.part < 0;
             const int Lq = MODE == BLOCKS ? p.g.q_tokens() : p.T;
             if (token >= 0) {
                 if (!direct)
-                    p.part_lse[(long long)u * p.rows + r] = lse2;
+                    p.part_lse[w.x.part * p.rows + r] = lse2;
                 else if (p.lse)
-                    p.lse[((long long)b * p.heads + h) * Lq + token] = lse2 * 0.6931471805599453f;
+                    p.lse[((long long)w.x.b * p.heads + w.x.h) * Lq + token] = lse2 * 0.6931471805599453f;
             }
-            __nv_bfloat16* orow = p.o + ((long long)b * Lq + token) * p.ldo + h * 128;
+            __nv_bfloat16* orow = p.o + ((long long)w.x.b * Lq + token) * p.ldo + w.x.h * 128;
             if (n == 0) {  // a list without keys; the join does not read rows whose sum is empty
                 if (direct && token >= 0)
                     for (int c = 0; c < 16; ++c) reinterpret_cast<uint4*>(orow)[c] = make_uint4(0, 0, 0, 0);
                 continue;
             }
-            float* prow = p.part_o + ((long long)u * p.rows + r) * 128;
+            float* prow = p.part_o + (w.x.part * p.rows + r) * 128;
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
                 uint32_t ov[32];
@@ -666,8 +738,8 @@ __global__ void __launch_bounds__(alist::THREADS, 1)
     }
 }
 
-// Joins the splits of one query row: O = sum_s w_s O_s, w_s = 2^(lse_s - lse).
-// One warp per row; a split without keys has lse -inf and is not read.
+// Joins the parts of one query row's list: O = sum_s w_s O_s, w_s = 2^(lse_s -
+// lse).  One warp per row; a part without keys has lse -inf and is not read.
 template <alist::Mode MODE>
 __global__ void __launch_bounds__(256) list_join_kernel(const __grid_constant__ ListParams p) {
     const int lane = threadIdx.x & 31;
@@ -676,37 +748,67 @@ __global__ void __launch_bounds__(256) list_join_kernel(const __grid_constant__ 
     if (row >= (long long)per * p.rows) return;
     const int unit = (int)(row / p.rows), r = (int)(row % p.rows);
     const int qt = unit % p.nqb, h = unit / p.nqb % p.heads, b = unit / p.nqb / p.heads;
-    int token, Lq;
-    if (MODE == alist::BLOCKS) {
-        const int nj = p.g.nq(2), ni = p.g.nq(1);
-        const int f = (qt / nj / ni) * p.g.qb[0] + r / (p.g.qb[2] * p.g.qb[1]);
-        const int i = (qt / nj % ni) * p.g.qb[1] + r / p.g.qb[2] % p.g.qb[1];
-        const int j = (qt % nj) * p.g.qb[2] + r % p.g.qb[2];
-        if (f >= p.g.q[0] || i >= p.g.q[1] || j >= p.g.q[2]) return;
-        token = (f * p.g.q[1] + i) * p.g.q[2] + j;
-        Lq = p.g.q_tokens();
-    } else {
-        token = qt * 128 + r;
-        Lq = p.T;
-        if (token >= Lq) return;
+    const int token = list_token<MODE>(p, qt, r);
+    if (token < 0) return;
+    const int Lq = MODE == alist::BLOCKS ? p.g.q_tokens() : p.T;
+    int s0 = 0, s1 = p.splits - 1;
+    bool inside = false;  // pages: the first part begins inside its range
+    if (MODE == alist::PAGES) {
+        uint32_t first = 0, total = 0, mine = 0;
+        for (int i = lane; i < p.B; i += 32) {
+            const uint32_t n = page_tiles(page_tokens(p, i));
+            total += n;
+            if (i < b) first += n;
+            if (i == b) mine = n;
+        }
+        first = __reduce_add_sync(0xffffffffu, first);
+        total = __reduce_add_sync(0xffffffffu, total);
+        mine = __reduce_add_sync(0xffffffffu, mine);
+        if (mine == 0) return;
+        // range that holds tile x: the largest r with floor(r total / ranges) <= x
+        const uint32_t ranges = page_ranges(p, total);
+        auto range_of = [&](uint32_t x) {
+            return (int)(((x + 1ull) * ranges + total - 1) / total) - 1;
+        };
+        s0 = range_of(first);
+        s1 = range_of(first + mine - 1);
+        if (s0 == s1) return;  // whole in one range: written by its unit
+        inside = (uint32_t)((unsigned long long)total * s0 / ranges) < first;
     }
-    auto at = [&](int s) { return ((long long)s * per + unit) * p.rows + r; };
+    auto at = [&](int s) {
+        if (MODE == alist::BLOCKS) return ((long long)s * per + unit) * p.rows + r;
+        const long long u = (long long)s * (p.nqb * p.heads) + h * p.nqb + qt;
+        return (u * 2 + (s == s0 && inside)) * p.rows + r;
+    };
+    // a lane per part for its lse, then all lanes add up the parts' rows, a few loads in flight
     float m = -INFINITY;
-    for (int s = lane; s < p.splits; s += 32) m = fmaxf(m, p.part_lse[at(s)]);
+    for (int s = s0 + lane; s <= s1; s += 32) m = fmaxf(m, p.part_lse[at(s)]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float total = 0.f;
-    for (int s = 0; s < p.splits; ++s) {
-        const float l = p.part_lse[at(s)];
-        if (l == -INFINITY) continue;
-        const float w = exp2f(l - m);
-        const float4 x = *reinterpret_cast<const float4*>(p.part_o + at(s) * 128 + lane * 4);
-        total += w;
-        acc.x += w * x.x;
-        acc.y += w * x.y;
-        acc.z += w * x.z;
-        acc.w += w * x.w;
+    for (int c = s0; c <= s1; c += 32) {
+        const float l = c + lane <= s1 ? p.part_lse[at(c + lane)] : -INFINITY;
+        const float w = l == -INFINITY ? 0.0f : exp2f(l - m);
+        const int n = min(32, s1 - c + 1);
+        for (int i = 0; i < n; i += 8) {
+            float4 x[8];
+            float wi[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                wi[j] = i + j < n ? __shfl_sync(0xffffffffu, w, (i + j) & 31) : 0.0f;
+                x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (wi[j] != 0.0f) x[j] = *reinterpret_cast<const float4*>(p.part_o + at(c + i + j) * 128 + lane * 4);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                total += wi[j];
+                acc.x += wi[j] * x[j].x;
+                acc.y += wi[j] * x[j].y;
+                acc.z += wi[j] * x[j].z;
+                acc.w += wi[j] * x[j].w;
+            }
+        }
     }
     const float inv = total == 0.f ? 0.f : 1.0f / total;
     uint2 out = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
@@ -729,15 +831,15 @@ namespace {
 // Splits of each list: the number that takes the least time in tile steps.  A
 // unit costs its tiles plus about three steps of filling and draining; a split
 // one also writes its fp32 rows, and the join reads them all again.
-int list_splits(long long per, int max_tiles, int rows) {
+int list_splits(long long per, long long max_tiles, int rows) {
     const int streams = 2 * alist::PLAN_SMS;
-    if (per >= 8 * streams) return 1;
+    if (per <= 0 || per >= 8 * streams) return 1;
     int best = 1;
     double least = 1e30;
-    for (int s = 1; s <= 64 && s <= max_tiles; ++s) {
+    for (int s = 1; s <= 2 * streams / per + 16 && s <= max_tiles; ++s) {
         const long long waves = (per * s + streams - 1) / streams;
         const double share = rows / 128.0;
-        const double cost = (double)waves * ((max_tiles + s - 1) / s + 3 + (s > 1 ? share : 0)) +
+        const double cost = (double)waves * ((max_tiles + s - 1) / s + 5 + (s > 1 ? share : 0)) +
                             (s > 1 ? 4 + 0.013 * share * per * s : 0);
         if (cost < least) {
             least = cost;
@@ -747,18 +849,16 @@ int list_splits(long long per, int max_tiles, int rows) {
     return best;
 }
 
-long long list_workspace(long long units, int rows, int splits) {
-    return splits == 1 ? 0 : units * splits * rows * 129ll * 4;
-}
+long long list_workspace(long long parts, int rows) { return parts * rows * 129ll * 4; }
 
 template <alist::Mode MODE>
 cudaError_t launch_list(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, ListParams& p, void* ws,
                         const LaunchCtx& ctx) {
     const long long per = (long long)p.nqb * p.heads * p.B;
-    p.units = (int)(per * p.splits);
+    p.units = MODE == alist::BLOCKS ? (int)(per * p.splits) : p.nqb * p.heads * p.splits;
     if (p.splits > 1) {
         p.part_o = reinterpret_cast<float*>(ws);
-        p.part_lse = p.part_o + (long long)p.units * p.rows * 128;
+        p.part_lse = p.part_o + (long long)p.units * (MODE == alist::BLOCKS ? 1 : 2) * p.rows * 128;
     }
     p.scale_log2 = 1.4426950408889634f / sqrtf(128.0f);
     p.wc.err = ctx.err;
@@ -828,9 +928,10 @@ bool pages_plan(int B, int heads, int T, int max_pages, int page_size, ListParam
     p->rows = T < 128 ? T : 128;
     p->max_pages = max_pages;
     list_groups(page_size, p);
-    const long long per = (long long)p->nqb * heads * B;
-    p->splits = list_splits(per, ((max_pages << p->log_sub) + p->E - 1) / p->E, p->rows);
-    return per * p->splits < (1ll << 31) - 1024;
+    const long long inner = (long long)p->nqb * heads;
+    const long long tiles = ((long long)max_pages << (p->log_sub + p->log_group)) / alist::KEYS + 1;
+    p->splits = list_splits(inner, tiles * B, p->rows);
+    return inner * p->splits < (1ll << 30);
 }
 
 }  // namespace
@@ -838,13 +939,21 @@ bool pages_plan(int B, int heads, int T, int max_pages, int page_size, ListParam
 long long attention_blocks_workspace(int B, int heads, const BlockGrid& g, int topk) {
     ListParams p{};
     if (!blocks_plan(B, heads, g, topk, &p)) return -1;
-    return list_workspace((long long)p.nqb * heads * B, p.rows, p.splits);
+    return p.splits == 1 ? 0 : list_workspace((long long)p.nqb * heads * B * p.splits, p.rows);
 }
 
 long long attention_paged_workspace(int B, int heads, int T, int max_pages, int page_size) {
     ListParams p{};
-    if (!pages_plan(B, heads, T, max_pages, page_size, &p)) return -1;
-    return list_workspace((long long)p.nqb * heads * B, p.rows, p.splits);
+    if (B == 0 || T == 0) return 0;
+    // sequences are launched up to MAX_SEQS at a time, one launch after the other in the same room
+    if (!pages_plan(B < alist::MAX_SEQS ? B : alist::MAX_SEQS, heads, T, max_pages, page_size, &p)) return -1;
+    long long need = p.splits == 1 ? 0 : list_workspace((long long)p.nqb * heads * p.splits * 2, p.rows);
+    if (B > alist::MAX_SEQS && B % alist::MAX_SEQS) {
+        if (!pages_plan(B % alist::MAX_SEQS, heads, T, max_pages, page_size, &p)) return -1;
+        const long long last = p.splits == 1 ? 0 : list_workspace((long long)p.nqb * heads * p.splits * 2, p.rows);
+        need = last > need ? last : need;
+    }
+    return need;
 }
 
 cudaError_t launch_attention_blocks(const void* q, long long ldq, const void* k, long long ldk, const void* v,
@@ -872,23 +981,29 @@ cudaError_t launch_attention_blocks(const void* q, long long ldq, const void* k,
 
 cudaError_t launch_attention_paged(const void* q, long long ldq, const KvPages& c, const int* lens, void* o,
                                    long long ldo, int B, int heads, int T, float* lse, void* ws, const LaunchCtx& ctx) {
-    ListParams p{};
-    if (!pages_plan(B, heads, T, c.max_pages, c.page_size, &p)) return cudaErrorInvalidValue;
-    p.table = c.table;
-    p.table_ld = c.table_ld;
-    p.num_pages = c.num_pages;
-    p.lens = lens;
-    p.o = reinterpret_cast<__nv_bfloat16*>(o);
-    p.ldo = ldo;
-    p.lse = lse;
     const uint64_t width = (uint64_t)heads * 128;
-    const uint32_t group = 1u << p.log_group;
-    CUtensorMap tq, tk, tv;
-    if (!make_tmap_3d(&tq, q, width, T, B, ldq, (uint64_t)ldq * T, 64, 128) ||
-        !make_tmap_3d(&tk, c.k, width, c.page_size, c.num_pages, c.token_stride, c.page_stride, 64, group) ||
-        !make_tmap_3d(&tv, c.v, width, c.page_size, c.num_pages, c.token_stride, c.page_stride, 64, group))
-        return cudaErrorInvalidValue;
-    return launch_list<alist::PAGES>(tq, tk, tv, p, ws, ctx);
+    for (int b0 = 0; b0 < B; b0 += alist::MAX_SEQS) {
+        const int n = B - b0 < alist::MAX_SEQS ? B - b0 : alist::MAX_SEQS;
+        ListParams p{};
+        if (!pages_plan(n, heads, T, c.max_pages, c.page_size, &p)) return cudaErrorInvalidValue;
+        p.table = c.table + b0 * c.table_ld;
+        p.table_ld = c.table_ld;
+        p.num_pages = c.num_pages;
+        p.lens = lens + b0;
+        p.o = reinterpret_cast<__nv_bfloat16*>(o) + (long long)b0 * T * ldo;
+        p.ldo = ldo;
+        p.lse = lse ? lse + (long long)b0 * heads * T : nullptr;
+        const uint32_t group = 1u << p.log_group;
+        const void* q0 = reinterpret_cast<const __nv_bfloat16*>(q) + (long long)b0 * T * ldq;
+        CUtensorMap tq, tk, tv;
+        if (!make_tmap_3d(&tq, q0, width, T, n, ldq, (uint64_t)ldq * T, 64, 128) ||
+            !make_tmap_3d(&tk, c.k, width, c.page_size, c.num_pages, c.token_stride, c.page_stride, 64, group) ||
+            !make_tmap_3d(&tv, c.v, width, c.page_size, c.num_pages, c.token_stride, c.page_stride, 64, group))
+            return cudaErrorInvalidValue;
+        const cudaError_t e = launch_list<alist::PAGES>(tq, tk, tv, p, ws, ctx);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace wan

@@ -1438,7 +1438,7 @@ bool block_grid_ok(const wan_block_grid* g, int B, int heads, wan::BlockGrid* ou
 bool kv_cache_ok(const wan_kv_cache* c, int heads, wan::KvPages* out) {
     *out = wan::KvPages{c->k, c->v, c->page_stride, c->token_stride, c->num_pages, c->page_size, c->table, c->table_ld, c->max_pages};
     if (!group_ok(c->page_size) || c->num_pages < 1 || c->max_pages < 1 || c->table_ld < c->max_pages) return false;
-    if ((int64_t)c->max_pages * c->page_size > (1 << 30)) return false;
+    if ((int64_t)c->max_pages * c->page_size > (1 << 29)) return false;
     if (!ld_ok(c->token_stride, heads) || c->page_stride % 8 || c->page_stride >= (1ll << 38)) return false;
     if (c->page_stride < (c->page_size - 1) * c->token_stride + 128ll * heads) return false;
     return aligned16({c->k, c->v});
