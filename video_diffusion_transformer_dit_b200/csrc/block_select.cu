@@ -8,15 +8,21 @@
 // of additions.  Computing them all in fp64 would cost more than reading q and k
 // (190 us against 62 us at the 480p pair's 24 x 336 x 624 scores), so rows of up
 // to 2048 blocks go in two stages:
-//   block_mean_kernel   one pass over q and k: fp64 means, their bf16 hi + lo
-//                       parts and their norms;
-//   block_score_kernel  scores from three bf16 products (hi hi + hi lo + lo hi) on
-//                       the tensor cores, fp32 sums; every score is within
-//                       SCORE_ERROR |q| |k| of its 64-bit value;
-//   block_topk_kernel   the topk-th best of a row by bisection; only blocks whose
-//                       score lies within the error of it are scored again, in
-//                       fp64, and ranked by that (none or a few per row).
+//   block_mean_kernel   one pass over q and k: fp64 means, the same scaled to unit
+//                       length in fp16, and their norms;
+//   block_score_kernel  unit products on the tensor cores times the key's norm:
+//                       within SCORE_ERROR |k| of the 64-bit score over |q|;
+//   block_topk_kernel   the topk-th best of a row by bisection; only blocks that
+//                       the error lets lie on either side of the border (seven or
+//                       so of several hundred) are scored again, in fp64, and
+//                       ranked by that.
+// (With hi + lo parts and three products fewer are scored again, but the products
+// and their operands cost more than that saves: 30 against 12 us of the pair's.)
 // Longer rows: block_score64_kernel and block_topk64_kernel, all in fp64.
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -27,20 +33,20 @@ namespace {
 constexpr int SCORE_Q = 32, SCORE_K = 64;  // fp64 score kernel: query x key blocks per CTA
 constexpr int K_PITCH = 129;               // doubles per staged mean (odd: column reads hit all banks)
 constexpr int MAX_FAST = 2048;             // key blocks of the two-stage path
-// Bound of a tensor-core score's error over |q| |k|: a bf16 rounding is off by
-// 2^-8, so lo misses 2^-16 of each factor and lo lo is another 2^-16 (4.6e-5 in
-// all); 384 fp32 additions, truncated, add at most 384 * 2^-23 (4.6e-5).
-constexpr float SCORE_ERROR = 1.220703125e-4f;  // 2^-13
-constexpr float SCORE_TINY = 1e-34f;            // below it products lose bits to underflow
+// Bound of a unit product's error: an fp16 rounding is off by 2^-11 of the element
+// (or by 2^-25 where it is subnormal), on either side: 2 * 2^-11 (1 + 2^-11) + 2 *
+// 2^-25 * sqrt(128); 128 fp32 additions, truncated, add at most 128 * 2^-23.
+constexpr float SCORE_ERROR = 1.007e-3f;
+constexpr float SCORE_TINY = 1e-36f;            // below it scores lose bits to underflow
 
-// Means of the blocks of q (first g.q_blocks() CTAs) and k, per head: fp64, bf16
-// hi | lo parts [256] and norm.  One CTA per block and 256-thread column slice,
+// Means of the blocks of q (first g.q_blocks() CTAs) and k, per head: fp64, fp16 of
+// unit length, and norm (NaN or infinite where a mean is).  One CTA per block and 256-thread column slice,
 // eight columns per thread; four tokens are added in fp32 before they join the
 // fp64 sum: bf16 has 8 significant bits, so a sum of four of them is exact in
 // fp32's 24 unless their exponents lie 14 apart.
 struct MeanOut {
     double* mean;           // [B, heads, blocks, 128]
-    __nv_bfloat16* parts;   // [B, heads, blocks, 256], null: not wanted
+    __half* unit;           // [B, heads, blocks, 128], null: not wanted
     float* norm;            // [B, heads, blocks]
 };
 __global__ void __launch_bounds__(256) block_mean_kernel(const __nv_bfloat16* __restrict__ q, long long ldq,
@@ -101,27 +107,31 @@ __global__ void __launch_bounds__(256) block_mean_kernel(const __nv_bfloat16* __
     const MeanOut& o = keys ? ok : oq;
     const long long at = ((long long)b * heads + (mine ? col / 128 : 0)) * (nF * nH * nW) + blk;
     const double count = (double)n;
-    float hi[8], lo[8], ss = 0.f;
+    double ss = 0.0;
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
         acc[c] /= count;
-        hi[c] = __bfloat162float(__float2bfloat16_rn((float)acc[c]));
-        lo[c] = (float)(acc[c] - (double)hi[c]);
-        ss += (float)acc[c] * (float)acc[c];
+        ss += acc[c] * acc[c];
     }
+    if (o.unit) {
 #pragma unroll
-    for (int x = 8; x > 0; x >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, x);
+        for (int x = 8; x > 0; x >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, x);
+    }
     if (!mine) return;
     double* dst = o.mean + at * 128 + col % 128;
 #pragma unroll
     for (int c = 0; c < 8; c += 2) *reinterpret_cast<double2*>(dst + c) = make_double2(acc[c], acc[c + 1]);
-    if (!o.parts) return;
-    __nv_bfloat16* parts = o.parts + at * 256 + col % 128;
-    *reinterpret_cast<uint4*>(parts) =
-        make_uint4(pack_bf16(hi[0], hi[1]), pack_bf16(hi[2], hi[3]), pack_bf16(hi[4], hi[5]), pack_bf16(hi[6], hi[7]));
-    *reinterpret_cast<uint4*>(parts + 128) =
-        make_uint4(pack_bf16(lo[0], lo[1]), pack_bf16(lo[2], lo[3]), pack_bf16(lo[4], lo[5]), pack_bf16(lo[6], lo[7]));
-    if ((threadIdx.x & 15) == 0) o.norm[at] = sqrtf(ss) * 1.0001f;
+    if (!o.unit) return;
+    const double norm = sqrt(ss);
+    const double inv = norm > 0.0 && norm < 1e300 ? 1.0 / norm : 0.0;
+    uint32_t u[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const __half2 h = __floats2half2_rn((float)(acc[2 * c] * inv), (float)(acc[2 * c + 1] * inv));
+        u[c] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *reinterpret_cast<uint4*>(o.unit + at * 128 + col % 128) = make_uint4(u[0], u[1], u[2], u[3]);
+    if ((threadIdx.x & 15) == 0) o.norm[at] = (float)norm;
 }
 
 // ---------------------------------------------------------------- two-stage path
@@ -132,32 +142,34 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
 }
 __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// scores[bh][i][j] = hi hi + hi lo + lo hi of the means' parts.  64 x 64 scores per
-// CTA, four warps of 32 x 32; both operands whole (K = 128) in shared memory, 512
-// bytes a row, 16-byte pieces swizzled by the row.  mma.sync and not tcgen05: the
-// products are a few microseconds of work in tiles too small to fill a 128-row
-// accumulator per head.
+// scores[bh][i][j] = (unit mean of q block i) . (unit mean of k block j) * |k j|,
+// rows `pitch` apart.  64 x 64 scores per CTA, four warps of 32 x 32; both operands
+// whole (K = 128) in shared memory, 256 bytes a row, 16-byte pieces swizzled by the
+// row.  mma.sync and not tcgen05: a few microseconds of work, in tiles too small
+// for a 128-row accumulator.
 constexpr int ST = 64;
-__global__ void __launch_bounds__(128) block_score_kernel(const __nv_bfloat16* __restrict__ qp, const __nv_bfloat16* __restrict__ kp,
-                                                          int nq, int nk, float* __restrict__ scores) {
-    extern __shared__ uint4 tile[];  // [2][ST][32]
+__global__ void __launch_bounds__(128) block_score_kernel(const __half* __restrict__ qu, const __half* __restrict__ ku,
+                                                          const float* __restrict__ kn, int nq, int nk, int pitch,
+                                                          float* __restrict__ scores) {
+    __shared__ uint4 tile[2 * ST * 16];
     const int q0 = blockIdx.y * ST, k0 = blockIdx.x * ST;
     const long long bh = blockIdx.z;
-    for (int i = threadIdx.x; i < 2 * ST * 32; i += 128) {
-        const int which = i / (ST * 32), r = i / 32 % ST, c = i % 32;
+#pragma unroll
+    for (int i = threadIdx.x; i < 2 * ST * 16; i += 128) {
+        const int which = i / (ST * 16), r = i / 16 % ST, c = i % 16;
         const int at = (which ? k0 : q0) + r, n = which ? nk : nq;
-        const __nv_bfloat16* src = (which ? kp : qp) + (bh * n + at) * 256 + c * 8;
-        tile[(which * ST + r) * 32 + (c ^ (r & 7))] = at < n ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+        const __half* src = (which ? ku : qu) + (bh * n + at) * 128 + c * 8;
+        tile[(which * ST + r) * 16 + (c ^ (r & 7))] = at < n ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
     }
     __syncthreads();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int m0 = (warp >> 1) * 32, n0 = (warp & 1) * 32;
-    const uint32_t sq = smem_u32(tile), sk = sq + ST * 512;
+    const uint32_t sq = smem_u32(tile), sk = sq + ST * 256;
     float acc[2][4][4];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -165,49 +177,37 @@ __global__ void __launch_bounds__(128) block_score_kernel(const __nv_bfloat16* _
         for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int c = 0; c < 4; ++c) acc[i][j][c] = 0.f;
-    // 8 x 8 matrices of a x4 load: rows lane & 7 (+ 8), 16-byte piece 2 kk (+ 1); part: 0 hi, 16 lo
-    auto load_a = [&](uint32_t (&r)[4], int row, int kk, int part) {
-        const int at = row + (lane & 15), c = part + 2 * kk + (lane >> 4);
-        ldmatrix4(r, sq + at * 512 + ((c ^ (at & 7)) << 4));
-    };
-    auto load_b = [&](uint32_t (&r)[4], int row, int kk, int part) {  // two n8 tiles
-        const int at = row + (lane & 7) + ((lane >> 4) << 3), c = part + 2 * kk + ((lane >> 3) & 1);
-        ldmatrix4(r, sk + at * 512 + ((c ^ (at & 7)) << 4));
-    };
-#pragma unroll 2
+#pragma unroll
     for (int kk = 0; kk < 8; ++kk) {
-        uint32_t ah[2][4], al[2][4], bh4[2][4], bl4[2][4];
+        // 8 x 8 matrices of an x4 load: A rows lane & 15, pieces 2 kk + (lane >> 4); B two n8 tiles
+        uint32_t a[2][4], b[2][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            load_a(ah[i], m0 + 16 * i, kk, 0);
-            load_a(al[i], m0 + 16 * i, kk, 16);
-            load_b(bh4[i], n0 + 16 * i, kk, 0);
-            load_b(bl4[i], n0 + 16 * i, kk, 16);
+            const int ra = m0 + 16 * i + (lane & 15), ca = 2 * kk + (lane >> 4);
+            ldmatrix4(a[i], sq + ra * 256 + ((ca ^ (ra & 7)) << 4));
+            const int rb = n0 + 16 * i + (lane & 7) + ((lane >> 4) << 3), cb = 2 * kk + ((lane >> 3) & 1);
+            ldmatrix4(b[i], sk + rb * 256 + ((cb ^ (rb & 7)) << 4));
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t h0 = bh4[j >> 1][(j & 1) * 2], h1 = bh4[j >> 1][(j & 1) * 2 + 1];
-                mma_16816(acc[i][j], ah[i], bl4[j >> 1][(j & 1) * 2], bl4[j >> 1][(j & 1) * 2 + 1]);
-                mma_16816(acc[i][j], al[i], h0, h1);
-                mma_16816(acc[i][j], ah[i], h0, h1);
-            }
+            for (int j = 0; j < 4; ++j) mma_16816(acc[i][j], a[i], b[j >> 1][(j & 1) * 2], b[j >> 1][(j & 1) * 2 + 1]);
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 4; ++j) {
+        const int col = k0 + n0 + 8 * j + (lane & 3) * 2;  // even, as the pitch is
+        if (col >= nk) continue;
+        const float s0 = __ldg(kn + bh * nk + col), s1 = col + 1 < nk ? __ldg(kn + bh * nk + col + 1) : 0.f;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int row = q0 + m0 + 16 * i + half * 8 + (lane >> 2);
-            if (row >= nq) continue;
-            float* dst = scores + (bh * nq + row) * nk;
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int col = k0 + n0 + 8 * j + (lane & 3) * 2;
-                if (col < nk) dst[col] = acc[i][j][half * 2];
-                if (col + 1 < nk) dst[col + 1] = acc[i][j][half * 2 + 1];
+            for (int half = 0; half < 2; ++half) {
+                const int row = q0 + m0 + 16 * i + half * 8 + (lane >> 2);
+                if (row < nq)
+                    *reinterpret_cast<float2*>(scores + (bh * nq + row) * pitch + col) =
+                        make_float2(acc[i][j][half * 2] * s0, acc[i][j][half * 2 + 1] * s1);
             }
-        }
+    }
 }
 
 // A score as a 64-bit key in the same order: NaN ranks with -inf, keys of
@@ -286,66 +286,123 @@ __global__ void __launch_bounds__(128) block_score64_kernel(const double* __rest
     }
 }
 
-// The topk best blocks of a row: one warp per row, NPL scores per lane in
-// registers (nk <= 32 NPL).  Bisection between the row's smallest and largest key
-// ends as soon as a threshold leaves exactly topk of them (a dozen steps).  Blocks
-// whose score lies within twice the error bound of the topk-th are ranked by their
-// fp64 scores, equal ones to the lower block.
+// The topk best blocks of a row: one warp per row, a lane holding the keys of NPL
+// consecutive blocks in registers (nk <= 32 NPL).  A threshold that leaves topk
+// keys is found by interpolation and bisection in turn (half a dozen counts).
+// With a_j the fp32 score of block j and d_j the bound of its error, the topk-th
+// best 64-bit score is at least L = min (a_j - d_j) over the topk best a_j and at
+// most U = max (a_j + d_j) over the topk-th and all others: blocks with a_j - d_j >
+// U are taken, those with a_j + d_j < L are not, and the close ones in between are
+// ranked by their fp64 scores, equal ones to the lower block.
 struct TopkParams {
-    const float* scores;            // [B heads nq, nk]
+    const float* scores;            // [B heads nq, pitch]
     const double *qm, *km;          // means
     const float *qn, *kn;           // their norms
     const uint8_t* mask;            // [nq, nk] or null
     unsigned long long* exact;      // [rows, nk]: used by rows with many close scores only
-    int nq, nk, topk;
-    long long rows;
+    int nq, nk, pitch, topk;
     int *blocks, *counts;
 };
 template <int NPL>
 __global__ void __launch_bounds__(128) block_topk_kernel(const __grid_constant__ TopkParams p) {
-    const int lane = threadIdx.x & 31;
-    const uint32_t below = (1u << lane) - 1;
-    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (row >= p.rows) return;
-    const int nk = p.nk;
-    const long long bh = row / p.nq;
-    const float* src = p.scores + row * nk;
-    const uint8_t* mrow = p.mask ? p.mask + (row - bh * p.nq) * nk : nullptr;
-    const float* kn = p.kn + bh * nk;
+    using Bits = typename std::conditional<(NPL > 32), unsigned long long, uint32_t>::type;
+    __shared__ int again[4][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int nk = p.nk, j0 = lane * NPL;  // the lane's first block
+    const long long bh = blockIdx.y;
+    const int i_q = blockIdx.x * 4 + warp;
+    if (i_q >= p.nq) return;
+    const long long row = bh * p.nq + i_q;
     uint32_t key[NPL];
-    uint32_t lo = ~0u, hi = 0;
-    float far = 0.f;  // largest key norm, NaN if one is
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-        const int j = i * 32 + lane;
-        key[i] = 0;
-        if (j < nk) {
-            key[i] = score_key32(__ldg(src + j));
-            if (mrow) {
-                const uint8_t m = __ldg(mrow + j);
-                key[i] = m == 0 ? 0u : m == 1 ? key[i] : ~0u;
-            }
-            const float x = __ldg(kn + j);
-            far = x > far || !(x == x) ? x : far;
-        }
-        if (key[i] != 0) lo = min(lo, key[i]);
-        hi = max(hi, key[i]);
+    for (int i = 0; i < NPL; i += 4) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j0 + i < nk) v = __ldg(reinterpret_cast<const float4*>(p.scores + row * p.pitch + j0 + i));
+        key[i] = j0 + i < nk ? score_key32(v.x) : 0u;
+        key[i + 1] = j0 + i + 1 < nk ? score_key32(v.y) : 0u;
+        key[i + 2] = j0 + i + 2 < nk ? score_key32(v.z) : 0u;
+        key[i + 3] = j0 + i + 3 < nk ? score_key32(v.w) : 0u;
     }
-    lo = __reduce_min_sync(0xffffffffu, lo);
-    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (p.mask) {
+        const uint8_t* mrow = p.mask + (long long)i_q * nk + j0;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+            const uint8_t m = j0 + i < nk ? __ldg(mrow + i) : 0;
+            key[i] = m == 0 ? 0u : m == 1 ? key[i] : ~0u;
+        }
+    }
     auto count = [&](uint32_t at) {  // keys >= at
         int n = 0;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) n += key[i] >= at;
         return (int)__reduce_add_sync(0xffffffffu, n);
     };
-    const int allowed = count(1);
+    const int allowed = count(1), always = p.mask ? count(~0u) : 0;
     const int take = min(p.topk, allowed);
-    // count(at) >= take, and == take unless equal keys lie at the border
+    int* dst = p.blocks + row * p.topk;
+    // the lane's picks to their places: ascending, after those of the lanes before
+    auto put = [&](Bits picks) {
+        const int mine = NPL > 32 ? __popcll(picks) : __popc((uint32_t)picks);
+        int to = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, to, o);
+            if (lane >= o) to += v;
+        }
+        to -= mine;
+        while (picks) {
+            const int i = NPL > 32 ? __ffsll((long long)picks) - 1 : __ffs((int)picks) - 1;
+            picks &= picks - 1;
+            dst[to++] = j0 + i;
+        }
+        for (int i = take + lane; i < p.topk; i += 32) dst[i] = -1;
+        if (lane == 0) p.counts[row] = take;
+    };
+    // picks among equals: the first `left` of the set bits, lanes in order
+    auto first_of = [&](Bits bits, int left) -> Bits {
+        const int mine = NPL > 32 ? __popcll(bits) : __popc((uint32_t)bits);
+        int before = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane >= o) before += v;
+        }
+        before -= mine;
+        Bits out = 0;
+        for (int n = before; bits && n < left; ++n) {
+            const Bits low = bits & (~bits + 1);
+            out |= low;
+            bits ^= low;
+        }
+        return out;
+    };
+    if (take == allowed || always >= take) {  // all that is allowed, or only blocks asked for
+        Bits bits = 0;
+        const uint32_t from = take == allowed ? 1u : ~0u;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) bits |= (Bits)(key[i] >= from) << i;
+        put(first_of(bits, take));
+        return;
+    }
+    // lo: a key that at least `take` keys reach; hi: one that fewer exceed
+    uint32_t lo = ~0u, hi = 0;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+        lo = min(lo, key[i] - 1);  // 0 wraps to the largest
+        hi = max(hi, key[i] == ~0u ? 0u : key[i]);
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo) + 1;
+    hi = __reduce_max_sync(0xffffffffu, hi);
     uint32_t at = lo;
-    int n_at = allowed;
-    while (n_at != take && lo < hi) {
-        const uint32_t mid = lo + ((hi - lo) >> 1) + 1;
+    int n_at = allowed, n_hi = always;
+    for (int step = 0; n_at != take && lo < hi; ++step) {
+        uint32_t mid = lo + ((hi - lo) >> 1) + 1;
+        if (step < 24) {  // between the scores; a place by the counts every other step
+            const float a = key32_score(lo), b = key32_score(hi);
+            const float part = step & 1 ? 0.5f : fminf(fmaxf((float)(n_at - take) / (float)(n_at - n_hi), 0.1f), 0.9f);
+            const uint32_t m = score_key32(a + part * (b - a));
+            if (m > lo && m <= hi) mid = m;
+        }
         const int n = count(mid);
         if (n >= take) {
             lo = mid;
@@ -353,159 +410,159 @@ __global__ void __launch_bounds__(128) block_topk_kernel(const __grid_constant__
             n_at = n;
         } else {
             hi = mid - 1;
+            n_hi = n;
         }
     }
-    int* dst = p.blocks + row * p.topk;
-    int written = 0;
-    auto put = [&](int i, bool pick) {
-        const unsigned picks = __ballot_sync(0xffffffffu, pick);
-        if (pick) dst[written + __popc(picks & below)] = i * 32 + lane;
-        written += __popc(picks);
-    };
-    // the topk-th score and the best one that is left out
-    uint32_t vk = ~0u, vn = 0;
+    // L, U and the close ones
+    const float* kn = p.kn + bh * nk + j0;
+    float L = INFINITY, U = -INFINITY;
+    uint32_t vk = ~0u;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) vk = min(vk, key[i] >= at ? key[i] : ~0u);
+    vk = __reduce_min_sync(0xffffffffu, vk);
+    bool number = p.qn[row] < INFINITY;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
-        if (key[i] >= at) vk = min(vk, key[i]);
-        else vn = max(vn, key[i]);
+        if (key[i] == 0 || key[i] == ~0u) continue;
+        const float d = fmaf(SCORE_ERROR, __ldg(kn + i), SCORE_TINY), a = key32_score(key[i]);
+        number = number && d < INFINITY;
+        if (key[i] >= at) L = fminf(L, a - d);
+        if (key[i] <= vk) U = fmaxf(U, a + d);
     }
-    vk = __reduce_min_sync(0xffffffffu, vk);
-    vn = __reduce_max_sync(0xffffffffu, vn);
+    number = __all_sync(0xffffffffu, number);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-        const float x = __shfl_xor_sync(0xffffffffu, far, o);
-        far = x > far || !(x == x) ? x : far;
+        L = fminf(L, __shfl_xor_sync(0xffffffffu, L, o));
+        U = fmaxf(U, __shfl_xor_sync(0xffffffffu, U, o));
     }
-    const float reach = 2.0f * (SCORE_ERROR * p.qn[row] * far + SCORE_TINY);
-    const float border = key32_score(vk);
-    if (take == 0 || vk == ~0u) {
-        // nothing, or blocks asked for alone: the lowest of them
-        int left = take;
+    if (!number) {  // a mean is not finite: all are close
+        L = -INFINITY;
+        U = INFINITY;
+    }
+    Bits sure = 0, close = 0;
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) {
-            const unsigned all = __ballot_sync(0xffffffffu, key[i] == ~0u);
-            put(i, key[i] == ~0u && __popc(all & below) < left);
-            left -= min(left, __popc(all));
+    for (int i = 0; i < NPL; ++i) {
+        if (key[i] == 0) continue;
+        const float d = key[i] == ~0u ? 0.f : fmaf(SCORE_ERROR, __ldg(kn + i), SCORE_TINY);
+        const float a = key32_score(key[i]);
+        const bool in = key[i] == ~0u || a - d > U;
+        sure |= (Bits)in << i;
+        close |= (Bits)(!in && !(a + d < L)) << i;
+    }
+    auto bits_of = [](Bits x) { return NPL > 32 ? __popcll(x) : __popc((uint32_t)x); };
+    const int n_sure = __reduce_add_sync(0xffffffffu, bits_of(sure));
+    const int n_close = __reduce_add_sync(0xffffffffu, bits_of(close));
+    const int need = take - n_sure;
+    if (n_close == need) {
+        put(sure | close);
+        return;
+    }
+    // fp64 keys: eight lanes per block, four blocks at a time; every lane gets its group's
+    const int sub = lane & 7;
+    const double2* qd = reinterpret_cast<const double2*>(p.qm + row * 128) + sub;
+    auto exact_key = [&](int j) {
+        const double2* kd = reinterpret_cast<const double2*>(p.km + (bh * nk + j) * 128) + sub;
+        double2 kv[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) kv[i] = __ldg(kd + 8 * i);
+        double s = 0.0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const double2 qv = __ldg(qd + 8 * i);
+            s = fma(qv.y, kv[i].y, fma(qv.x, kv[i].x, s));
         }
-    } else if (n_at == take && (vn == 0 || border - key32_score(vn) > reach)) {
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) put(i, key[i] >= at);
-    } else {
-        // close: 1 (ranked again); 2: taken for sure (also when reach is not a number: all are close)
-        auto kind = [&](uint32_t k) -> int {
-            if (k == 0) return 0;
-            if (k == ~0u) return 2;
-            const float s = key32_score(k);
-            return s > border + reach ? 2 : s < border - reach ? 0 : 1;
-        };
-        int close = 0, sure = 0;
+        for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        return score_key(s);
+    };
+    if (n_close <= 32) {
+        // lane n ranks the n-th close block among all of them
+        const int mine = bits_of(close);
+        int first = mine;
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) {
-            const int x = kind(key[i]);
-            close += x == 1;
-            sure += x == 2;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, first, o);
+            if (lane >= o) first += v;
         }
-        close = __reduce_add_sync(0xffffffffu, close);
-        sure = __reduce_add_sync(0xffffffffu, sure);
-        const double* qd = p.qm + row * 128 + lane * 4;
-        const double qx[4] = {qd[0], qd[1], qd[2], qd[3]};
-        auto exact_key = [&](int j) {  // all lanes: 64-bit key of block j
-            const double2* kd = reinterpret_cast<const double2*>(p.km + (bh * nk + j) * 128 + lane * 4);
-            const double2 k0 = __ldg(kd), k1 = __ldg(kd + 1);
-            double s = fma(qx[3], k1.y, fma(qx[2], k1.x, fma(qx[1], k0.y, qx[0] * k0.x)));
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            return score_key(s);
-        };
-        if (close <= 32) {
-            // lane n holds the n-th close block
-            unsigned long long mine = 0;
-            int n = 0;
-#pragma unroll
-            for (int i = 0; i < NPL; ++i) {
-                unsigned here = __ballot_sync(0xffffffffu, kind(key[i]) == 1);
-                while (here) {
-                    const int l = __ffs(here) - 1;
-                    here &= here - 1;
-                    const unsigned long long k = exact_key(i * 32 + l);
-                    if (lane == n) mine = k;
-                    ++n;
-                }
-            }
-            int better = 0;
-            for (int l = 0; l < close; ++l) {
-                const unsigned long long k = __shfl_sync(0xffffffffu, mine, l);
-                better += k > mine || (k == mine && l < lane);
-            }
-            const unsigned chosen = __ballot_sync(0xffffffffu, lane < close && better < take - sure);
-            int seen = 0;
-#pragma unroll
-            for (int i = 0; i < NPL; ++i) {
-                const int x = kind(key[i]);
-                const unsigned here = __ballot_sync(0xffffffffu, x == 1);
-                put(i, x == 2 || (x == 1 && (chosen >> ((seen + __popc(here & below)) & 31) & 1)));
-                seen += __popc(here);
-            }
-        } else {
-            // many close scores (equal blocks, infinities): all fp64 keys through memory
-            unsigned long long* ek = p.exact + row * nk;
-            unsigned long long lo64 = ~0ull, hi64 = 0;
+        first -= mine;
+        Bits rest = close;
+        for (int n = first; rest; ++n) {
+            const Bits low = rest & (~rest + 1);
+            again[warp][n] = j0 + bits_of(low - 1);
+            rest ^= low;
+        }
+        __syncwarp();
+        unsigned long long k = 0;
 #pragma unroll 1
-            for (int i0 = 0; i0 < nk; i0 += 32) {
-                const int j = i0 + lane;
-                uint32_t k32 = 0;
+        for (int c = 0; c < n_close; c += 4) {
+            const unsigned long long e = exact_key(again[warp][min(c + (lane >> 3), n_close - 1)]);
+            const unsigned long long got = __shfl_sync(0xffffffffu, e, (lane & 3) * 8);
+            if (lane >= c && lane < c + 4) k = got;  // c is a multiple of 4: lane & 3 == lane - c
+        }
+        int better = 0;
+        for (int l = 0; l < n_close; ++l) {
+            const unsigned long long other = __shfl_sync(0xffffffffu, k, l);
+            better += other > k || (other == k && l < lane);
+        }
+        const unsigned chosen = __ballot_sync(0xffffffffu, lane < n_close && better < need);
+        rest = close;
+        for (int n = first; rest; ++n) {
+            const Bits low = rest & (~rest + 1);
+            if (chosen >> n & 1) sure |= low;
+            rest ^= low;
+        }
+        put(sure);
+        return;
+    }
+    // many close scores (equal blocks, infinities): fp64 keys through memory
+    unsigned long long* ek = p.exact + row * nk;
+    unsigned long long lo64 = ~0ull, hi64 = 0;
+#pragma unroll 1
+    for (int c = 0; c < nk; c += 4) {
+        const int j = min(c + (lane >> 3), nk - 1);
+        const unsigned long long e = exact_key(j);
+        if (sub == 0) ek[j] = e;
+    }
+    __syncwarp();
+#pragma unroll 1
+    for (int i = 0; i < NPL; ++i)
+        if (close >> i & 1) {
+            lo64 = min(lo64, ek[j0 + i]);
+            hi64 = max(hi64, ek[j0 + i]);
+        }
 #pragma unroll
-                for (int i = 0; i < NPL; ++i)
-                    if (i * 32 == i0) k32 = key[i];
-                const int x = kind(k32);
-                unsigned long long k = x == 2 ? ~0ull : 0ull;
-                unsigned here = __ballot_sync(0xffffffffu, x == 1);
-                while (here) {
-                    const int l = __ffs(here) - 1;
-                    here &= here - 1;
-                    const unsigned long long e = exact_key(i0 + l);
-                    if (lane == l) k = e;
-                }
-                if (j < nk) ek[j] = k;
-                if (k) lo64 = min(lo64, k);
-                hi64 = max(hi64, k);
-            }
-            __syncwarp();
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                lo64 = min(lo64, __shfl_xor_sync(0xffffffffu, lo64, o));
-                hi64 = max(hi64, __shfl_xor_sync(0xffffffffu, hi64, o));
-            }
-            auto count64 = [&](unsigned long long v) {
-                int n = 0;
-                for (int j = lane; j < nk; j += 32) n += ek[j] >= v;
-                return (int)__reduce_add_sync(0xffffffffu, n);
-            };
-            unsigned long long at64 = lo64;
-            int n64 = close + sure;
-            while (n64 != take && lo64 < hi64) {
-                const unsigned long long mid = lo64 + ((hi64 - lo64) >> 1) + 1;
-                const int n = count64(mid);
-                if (n >= take) {
-                    lo64 = mid;
-                    at64 = mid;
-                    n64 = n;
-                } else {
-                    hi64 = mid - 1;
-                }
-            }
-            int ties = n64 == take ? take : take - count64(at64 + 1);  // at64 < ~0: fewer than take are sure
-            for (int i0 = 0; i0 < nk; i0 += 32) {
-                const int j = i0 + lane;
-                const unsigned long long k = j < nk ? ek[j] : 0ull;
-                const unsigned equal = __ballot_sync(0xffffffffu, k == at64 && k != 0);
-                put(i0 / 32, k > at64 || (k == at64 && k != 0 && __popc(equal & below) < ties));
-                ties -= min(ties, __popc(equal));
-            }
+    for (int o = 16; o > 0; o >>= 1) {
+        lo64 = min(lo64, __shfl_xor_sync(0xffffffffu, lo64, o));
+        hi64 = max(hi64, __shfl_xor_sync(0xffffffffu, hi64, o));
+    }
+    auto reach64 = [&](unsigned long long v) -> Bits {  // close blocks with keys >= v
+        Bits bits = 0;
+#pragma unroll 1
+        for (int i = 0; i < NPL; ++i)
+            if (close >> i & 1) bits |= (Bits)(ek[j0 + i] >= v) << i;
+        return bits;
+    };
+    auto count64 = [&](unsigned long long v) { return (int)__reduce_add_sync(0xffffffffu, bits_of(reach64(v))); };
+    unsigned long long at64 = lo64;
+    int n64 = n_close;
+    while (n64 != need && lo64 < hi64) {
+        const unsigned long long mid = lo64 + ((hi64 - lo64) >> 1) + 1;
+        const int n = count64(mid);
+        if (n >= need) {
+            lo64 = mid;
+            at64 = mid;
+            n64 = n;
+        } else {
+            hi64 = mid - 1;
         }
     }
-    for (int i = written + lane; i < p.topk; i += 32) dst[i] = -1;
-    if (lane == 0) p.counts[row] = take;
+    if (n64 == need) {
+        put(sure | reach64(at64));
+    } else {  // equal scores at the border: the lower blocks
+        const Bits above = reach64(at64 + 1), equal = reach64(at64) & ~above;
+        const int n_above = __reduce_add_sync(0xffffffffu, bits_of(above));
+        put(sure | above | first_of(equal, need - n_above));
+    }
 }
 
 // Longer rows: one CTA per row, fp64 keys in shared memory, bisected the same way.
@@ -601,13 +658,12 @@ __global__ void __launch_bounds__(256) block_topk64_kernel(const unsigned long l
     if (tid == 0) counts[row] = take;
 }
 
-constexpr int SCORE_SMEM = 2 * ST * 512;
 constexpr int SCORE64_SMEM = (128 * SCORE_Q + SCORE_K * K_PITCH) * 8;
 constexpr int TOPK64_SMEM = 225 * 1024;
 
 template <int NPL>
-void topk(const TopkParams& p, cudaStream_t stream) {
-    block_topk_kernel<NPL><<<(unsigned)((p.rows + 3) / 4), 128, 0, stream>>>(p);
+void topk(const TopkParams& p, long long bh, cudaStream_t stream) {
+    block_topk_kernel<NPL><<<dim3((p.nq + 3) / 4, (unsigned)bh), 128, 0, stream>>>(p);
 }
 
 }  // namespace
@@ -616,14 +672,13 @@ int block_select_max_blocks() { return TOPK64_SMEM / 8; }
 
 long long block_select_workspace(int B, int heads, const BlockGrid& g) {
     const long long nq = g.q_blocks(), nk = g.k_blocks();
-    const long long each = nk <= MAX_FAST ? (nq + nk) * (128 * 8 + 256 * 2 + 4) + nq * nk * 12 : (nq + nk) * 128 * 8 + nq * nk * 8;
-    return (long long)B * heads * each + 64;
+    const long long means = (nq + nk) * 128 * 8 + nq * nk * 8;
+    const long long fast = nk <= MAX_FAST ? (nq + nk) * (128 * 2 + 4) + nq * ((nk + 3) / 4 * 4) * 4 : 0;
+    return (long long)B * heads * (means + fast) + 64;
 }
 
 cudaError_t init_block_select_attributes() {
-    cudaError_t e = cudaFuncSetAttribute(block_score_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SCORE_SMEM);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(block_score64_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SCORE64_SMEM);
+    cudaError_t e = cudaFuncSetAttribute(block_score64_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SCORE64_SMEM);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(block_topk64_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, TOPK64_SMEM);
     return e;
@@ -635,19 +690,20 @@ cudaError_t launch_block_select(const void* q, long long ldq, const void* k, lon
     const int nq = g.q_blocks(), nk = g.k_blocks();
     const long long bh = (long long)B * heads, rows = bh * nq;
     const bool fast = nk <= MAX_FAST;
-    // workspace: 8-byte values first, then 16-byte aligned parts, then fp32
+    // workspace: 8-byte values first, then the 16-byte aligned fp16 units and fp32 rows
     double* qm = reinterpret_cast<double*>(ws);
     double* km = qm + bh * nq * 128;
     unsigned long long* keys = reinterpret_cast<unsigned long long*>(km + bh * nk * 128);  // [rows, nk]
     MeanOut oq{qm, nullptr, nullptr}, ok{km, nullptr, nullptr};
     float* scores = nullptr;
+    const int pitch = (nk + 3) / 4 * 4;
     if (fast) {
         uintptr_t at = (reinterpret_cast<uintptr_t>(keys + rows * nk) + 15) & ~uintptr_t(15);
-        oq.parts = reinterpret_cast<__nv_bfloat16*>(at);
-        ok.parts = oq.parts + bh * nq * 256;
-        oq.norm = reinterpret_cast<float*>(ok.parts + bh * nk * 256);
+        oq.unit = reinterpret_cast<__half*>(at);
+        ok.unit = oq.unit + bh * nq * 128;
+        scores = reinterpret_cast<float*>(ok.unit + bh * nk * 128);
+        oq.norm = scores + rows * pitch;
         ok.norm = oq.norm + bh * nq;
-        scores = ok.norm + bh * nk;
     }
     const int vecs = heads * 16;
     const int threads = vecs < 256 ? (vecs + 31) / 32 * 32 : 256;
@@ -655,15 +711,16 @@ cudaError_t launch_block_select(const void* q, long long ldq, const void* k, lon
     block_mean_kernel<<<dim3(nq + nk, slices, B), threads, 0, ctx.stream>>>(
         reinterpret_cast<const __nv_bfloat16*>(q), ldq, reinterpret_cast<const __nv_bfloat16*>(k), ldk, heads, g, oq, ok);
     if (fast) {
-        block_score_kernel<<<dim3((nk + ST - 1) / ST, (nq + ST - 1) / ST, (unsigned)bh), 128, SCORE_SMEM, ctx.stream>>>(
-            oq.parts, ok.parts, nq, nk, scores);
-        const TopkParams p{scores, qm, km, oq.norm, ok.norm, mask, keys, nq, nk, topk_, rows, blocks, counts};
+        block_score_kernel<<<dim3((nk + ST - 1) / ST, (nq + ST - 1) / ST, (unsigned)bh), 128, 0, ctx.stream>>>(
+            oq.unit, ok.unit, ok.norm, nq, nk, pitch, scores);
+        const TopkParams p{scores, qm, km, oq.norm, ok.norm, mask, keys, nq, nk, pitch, topk_, blocks, counts};
         const int per_lane = (nk + 31) / 32;
-        if (per_lane <= 4) topk<4>(p, ctx.stream);
-        else if (per_lane <= 12) topk<12>(p, ctx.stream);
-        else if (per_lane <= 20) topk<20>(p, ctx.stream);
-        else if (per_lane <= 32) topk<32>(p, ctx.stream);
-        else topk<64>(p, ctx.stream);
+        if (per_lane <= 4) topk<4>(p, bh, ctx.stream);
+        else if (per_lane <= 12) topk<12>(p, bh, ctx.stream);
+        else if (per_lane <= 20) topk<20>(p, bh, ctx.stream);
+        else if (per_lane <= 24) topk<24>(p, bh, ctx.stream);
+        else if (per_lane <= 32) topk<32>(p, bh, ctx.stream);
+        else topk<64>(p, bh, ctx.stream);
     } else {
         block_score64_kernel<<<dim3((nk + SCORE_K - 1) / SCORE_K, (nq + SCORE_Q - 1) / SCORE_Q, (unsigned)bh), 128,
                                SCORE64_SMEM, ctx.stream>>>(qm, km, mask, nq, nk, keys);
