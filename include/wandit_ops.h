@@ -199,7 +199,7 @@ typedef struct {
  * (q_out is written for every t < count[b] with start[b] >= 0).  Two sequences
  * that share a page must not write the same place.
  * Errors before any launch: WAN_EINVAL for a null pointer, WAN_ESHAPE for B, T <
- * 0, heads <= 0, a RoPE split that is not even with sum 128, H, W <= 0, theta <=
+ * 0, heads outside [1, 96], a RoPE split that is not even with sum 128, H, W <= 0, theta <=
  * 0, strides or pointers (k, v, q, q_out, the cache, gains) that are not
  * 16-byte aligned, a leading dimension or token stride below 128 * heads, a
  * page stride that lets pages overlap, or a cache outside the limits above.   */

@@ -109,7 +109,7 @@ def test_kv_append_refuses(lib):
         assert call(**kw) == EINVAL, kw
     for c in BAD_CACHES:
         assert call(c=cache(**c)) == ESHAPE, c
-    for kw in (dict(B=-1), dict(T=-1), dict(heads=0), dict(heads=3), dict(ldk=128), dict(ldv=252), dict(ldq=0), dict(ldqo=260),
+    for kw in (dict(B=-1), dict(T=-1), dict(heads=0), dict(heads=3), dict(heads=97, ldk=12416, ldv=12416, ldq=12416, ldqo=12416, c=cache(token_stride=12416, page_stride=64 * 12416)), dict(ldk=128), dict(ldv=252), dict(ldq=0), dict(ldqo=260),
                dict(k=ODD), dict(v=ODD), dict(q=ODD), dict(q_out=ODD), dict(k_gain=ODD), dict(q_gain=ODD), dict(H=0), dict(W=-1),
                dict(split=(44, 42, 41)), dict(split=(43, 43, 42)), dict(split=(130, -2, 0)), dict(theta=0.0),
                dict(theta=float("nan"))):

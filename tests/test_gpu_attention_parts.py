@@ -267,6 +267,10 @@ APPEND = [  # B, T, heads, (H, W), page, first places, counts, norm
     (2, 130, 12, (30, 52), 64, [1500, 7], [130, 129], True),
     (2, 9, 40, (4, 4), 128, [120, 250], None, False),
     (1, 20, 3, (5, 7), 32, [70], [99], True),                    # a count above T is T
+    (2, 700, 5, (9, 11), 16, [0, 333], [700, 651], True),        # several rows per warp
+    (2, 37, 17, (3, 4), 32, [9, 100], None, True),               # two warps per row
+    (3, 800, 33, (6, 7), 64, [0, 5, 900], [800, 1, 799], True),  # four
+    (1, 70, 96, (5, 5), 16, [3], None, True),                    # eight
 ]
 
 

@@ -9,6 +9,7 @@ there is no fallback path.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 from typing import Dict, Optional
 
@@ -483,74 +484,99 @@ def op_attention_ptr(q, ldq, k, ldk, v, ldv, o, ldo, B, heads, Lq, Lk, stream=No
 
 
 # ---------------------------------------------------------------- attention over parts of the sequence
-def _rows(name, t, dtype=None):
-    """A [B, L, D] tensor whose samples follow each other (row (b, l) at (b * L + l) * ld): its ld."""
+# These calls are made per layer and per token, where the host's time counts: sizes that follow
+# from the geometry alone are worked out once per geometry (lru_cache), tensors are looked at once.
+def _rows(name, t, B, L, D, device) -> int:
+    """Leading dimension of a bf16 tensor [B, L, D] whose row (b, l) lies at (b * L + l) * ld."""
     import torch
-    if t.dim() != 3 or t.dtype != (dtype or torch.bfloat16) or not t.is_cuda:
-        raise ValueError(f"{name}: a CUDA tensor [B, L, D] of {dtype or torch.bfloat16} is needed, "
-                         f"got {tuple(t.shape)} {t.dtype} on {t.device}")
-    ld = t.stride(1) if t.shape[1] > 1 else t.stride(0) if t.shape[0] > 1 and t.shape[1] == 1 else t.shape[2]
-    if t.stride(2) != 1 or (t.shape[0] > 1 and t.shape[1] > 1 and t.stride(0) != t.shape[1] * ld):
-        raise ValueError(f"{name}: rows must be dense and samples follow each other, got strides {t.stride()}")
+    shape, st = t.shape, t.stride()
+    if t.dtype is not torch.bfloat16 or len(shape) != 3 or shape[0] != B or shape[1] != L or shape[2] != D or \
+            t.device != device or device.type != "cuda":
+        raise ValueError(f"{name}: a bf16 CUDA tensor [{B}, {L}, {D}] on {device} is needed, "
+                         f"got {tuple(shape)} {t.dtype} on {t.device}")
+    ld = st[1] if L > 1 else st[0] if B > 1 and L == 1 else D
+    if st[2] != 1 or (B > 1 and L > 1 and st[0] != L * ld):
+        raise ValueError(f"{name}: rows must be dense and samples follow each other, got strides {st}")
     return ld
 
 
 def _dense(name, t, shape, dtype, device):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name}: a contiguous {dtype} tensor {tuple(shape)} on {device} is needed, "
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name}: a contiguous {dtype} tensor {shape} on {device} is needed, "
                          f"got {tuple(t.shape)} {t.dtype} on {t.device}")
-    return t
 
 
 def _block_grid(q_grid, k_grid, q_block, k_block) -> wan_block_grid:
     return wan_block_grid(*(int(n) for d in (q_grid, k_grid, q_block, k_block) for n in d))
 
 
-def _blocks_of(grid, block) -> int:
-    n = 1
-    for g, b in zip(grid, block):
-        n *= -(-g // b)
-    return n
+class _BlockPlan:
+    """What the block calls derive from their sizes."""
+
+    def __init__(self, B, heads, q_grid, k_grid, q_block, k_block, topk):
+        def count(grid, block):
+            n = 1
+            for g, b in zip(grid, block):
+                n *= -(-g // b) if b > 0 else 0
+            return n
+        self.grid = _block_grid(q_grid, k_grid, q_block, k_block)
+        self.ref = C.byref(self.grid)
+        self.Lq, self.Lk = (g[0] * g[1] * g[2] for g in (q_grid, k_grid))
+        self.nq, self.nk = count(q_grid, q_block), count(k_grid, k_block)
+        self.select_bytes = lib().wan_op_block_select_workspace(B, heads, self.ref)
+        self.attend_bytes = lib().wan_op_attention_blocks_workspace(B, heads, self.ref, topk)
 
 
-class _op_device:
+@functools.lru_cache(maxsize=256)
+def _block_plan(B, heads, q_grid, k_grid, q_block, k_block, topk) -> _BlockPlan:
+    return _BlockPlan(B, heads, q_grid, k_grid, q_block, k_block, topk)
+
+
+@functools.lru_cache(maxsize=256)
+def _paged_bytes(B, heads, T, page_stride, token_stride, num_pages, page_size, table_ld, max_pages) -> int:
+    c = wan_kv_cache(k=16, v=16, page_stride=page_stride, token_stride=token_stride, num_pages=num_pages,
+                     page_size=page_size, table=16, table_ld=table_ld, max_pages=max_pages)
+    return lib().wan_op_attention_paged_workspace(B, heads, T, C.byref(c))
+
+
+class _on:
     """The tensors' device and the launch stream made current for a call: buffers that the call allocates
-    belong to the stream that uses them."""
+    belong to the stream that uses them.  Gives the stream's handle."""
 
     def __init__(self, device, stream):
         import torch
-        self._enter = []
-        self._device = device
-        if device.index is not None and device.index != torch.cuda.current_device():
-            self._enter.append(torch.cuda.device(device))
+        self.enter = []
+        if device.index != torch.cuda.current_device():
+            self.enter.append(torch.cuda.device(device))
         if stream is not None:
             s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
-            self._enter.append(torch.cuda.stream(s))
+            self.enter.append(torch.cuda.stream(s))
 
     def __enter__(self):
-        for c in self._enter:
+        for c in self.enter:
             c.__enter__()
-        self.stream = _stream()
-        return self
+        return _stream()
 
     def __exit__(self, *exc):
-        for c in reversed(self._enter):
+        for c in reversed(self.enter):
             c.__exit__(*exc)
 
-    def scratch(self, nbytes, given):
-        """The caller's workspace, or a new one."""
-        import torch
-        if given is not None or nbytes <= 0:
-            return given
-        return torch.empty(nbytes, dtype=torch.uint8, device=self._device)
 
-
-def _nbytes(t) -> int:
-    return 0 if t is None else t.numel() * t.element_size()
+def _scratch(nbytes, given, device):
+    """(pointer, bytes, tensor) of the caller's workspace or of a new one."""
+    import torch
+    if given is None:
+        if nbytes <= 0:
+            return None, 0, None
+        given = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return given.data_ptr(), nbytes, given
+    if given.device != device or not given.is_contiguous():
+        raise ValueError(f"workspace: a contiguous tensor on {device} is needed, got one on {given.device}")
+    return given.data_ptr(), given.numel() * given.element_size(), given
 
 
 def op_block_select_workspace(B, heads, q_grid, k_grid, q_block, k_block) -> int:
-    return lib().wan_op_block_select_workspace(B, heads, C.byref(_block_grid(q_grid, k_grid, q_block, k_block)))
+    return _block_plan(B, heads, tuple(q_grid), tuple(k_grid), tuple(q_block), tuple(k_block), 1).select_bytes
 
 
 def op_block_select(q, k, heads, q_grid, k_grid, q_block, k_block, topk, mask=None, blocks=None, counts=None,
@@ -560,34 +586,30 @@ def op_block_select(q, k, heads, q_grid, k_grid, q_block, k_block, topk, mask=No
     key blocks] or None.  Returns (blocks int32 [B, heads, query blocks, topk], counts int32 [B, heads, query
     blocks]).  Buffers that are not given are allocated."""
     import torch
-    B, nq, nk, dev = q.shape[0], _blocks_of(q_grid, q_block), _blocks_of(k_grid, k_block), q.device
-    ldq, ldk = _rows("q", q), _rows("k", k)
-    _tokens_match("q", q, B, q_grid, heads, dev)
-    _tokens_match("k", k, B, k_grid, heads, dev)
+    B, dev = q.shape[0], q.device
+    p = _block_plan(B, heads, tuple(q_grid), tuple(k_grid), tuple(q_block), tuple(k_block), topk)
+    ldq, ldk = _rows("q", q, B, p.Lq, heads * 128, dev), _rows("k", k, B, p.Lk, heads * 128, dev)
     if mask is not None:
-        _dense("mask", mask, (nq, nk), torch.uint8, dev)
-    g = _block_grid(q_grid, k_grid, q_block, k_block)
-    with _op_device(dev, stream) as on:
+        _dense("mask", mask, (p.nq, p.nk), torch.uint8, dev)
+    with _on(dev, stream) as st:
         if blocks is None:
-            blocks = torch.empty((B, heads, nq, max(topk, 0)), dtype=torch.int32, device=dev)
+            blocks = torch.empty((B, heads, p.nq, max(topk, 0)), dtype=torch.int32, device=dev)
+        else:
+            _dense("blocks", blocks, (B, heads, p.nq, topk), torch.int32, dev)
         if counts is None:
-            counts = torch.empty((B, heads, nq), dtype=torch.int32, device=dev)
-        _dense("blocks", blocks, (B, heads, nq, topk), torch.int32, dev)
-        _dense("counts", counts, (B, heads, nq), torch.int32, dev)
-        ws = on.scratch(lib().wan_op_block_select_workspace(B, heads, C.byref(g)), workspace)
-        _check(lib().wan_op_block_select(_ptr(q), ldq, _ptr(k), ldk, B, heads, C.byref(g), _ptr(mask), topk, _ptr(blocks),
-                                         _ptr(counts), _ptr(ws), _nbytes(ws), on.stream), "wan_op_block_select")
+            counts = torch.empty((B, heads, p.nq), dtype=torch.int32, device=dev)
+        else:
+            _dense("counts", counts, (B, heads, p.nq), torch.int32, dev)
+        if B == 0:
+            return blocks, counts
+        ws, nbytes, _keep = _scratch(p.select_bytes, workspace, dev)
+        _check(lib().wan_op_block_select(q.data_ptr(), ldq, k.data_ptr(), ldk, B, heads, p.ref, _ptr(mask), topk,
+                                         blocks.data_ptr(), counts.data_ptr(), ws, nbytes, st), "wan_op_block_select")
     return blocks, counts
 
 
-def _tokens_match(name, t, B, grid, heads, device):
-    if t.shape[0] != B or t.shape[1] != grid[0] * grid[1] * grid[2] or t.shape[2] != heads * 128 or t.device != device:
-        raise ValueError(f"{name}: [{B}, {grid[0] * grid[1] * grid[2]}, {heads * 128}] on {device} is needed, "
-                         f"got {tuple(t.shape)} on {t.device}")
-
-
 def op_attention_blocks_workspace(B, heads, q_grid, k_grid, q_block, k_block, topk) -> int:
-    return lib().wan_op_attention_blocks_workspace(B, heads, C.byref(_block_grid(q_grid, k_grid, q_block, k_block)), topk)
+    return _block_plan(B, heads, tuple(q_grid), tuple(k_grid), tuple(q_block), tuple(k_block), topk).attend_bytes
 
 
 def op_attention_blocks(q, k, v, heads, q_grid, k_grid, q_block, k_block, blocks, counts, out=None, lse=None,
@@ -596,44 +618,43 @@ def op_attention_blocks(q, k, v, heads, q_grid, k_grid, q_block, k_block, blocks
     blocks int32 [B, heads, query blocks, topk], counts int32 [B, heads, query blocks]; lse f32 [B, heads, query
     tokens] is filled if given.  Returns out, bf16 [B, query tokens, D]."""
     import torch
-    B, nq, topk, dev = q.shape[0], _blocks_of(q_grid, q_block), blocks.shape[-1], q.device
-    Lq = q_grid[0] * q_grid[1] * q_grid[2]
-    ldq, ldk, ldv = _rows("q", q), _rows("k", k), _rows("v", v)
-    _tokens_match("q", q, B, q_grid, heads, dev)
-    _tokens_match("k", k, B, k_grid, heads, dev)
-    _tokens_match("v", v, B, k_grid, heads, dev)
-    _dense("blocks", blocks, (B, heads, nq, topk), torch.int32, dev)
-    _dense("counts", counts, (B, heads, nq), torch.int32, dev)
+    B, topk, dev, D = q.shape[0], blocks.shape[-1], q.device, heads * 128
+    p = _block_plan(B, heads, tuple(q_grid), tuple(k_grid), tuple(q_block), tuple(k_block), topk)
+    ldq, ldk, ldv = _rows("q", q, B, p.Lq, D, dev), _rows("k", k, B, p.Lk, D, dev), _rows("v", v, B, p.Lk, D, dev)
+    _dense("blocks", blocks, (B, heads, p.nq, topk), torch.int32, dev)
+    _dense("counts", counts, (B, heads, p.nq), torch.int32, dev)
     if lse is not None:
-        _dense("lse", lse, (B, heads, Lq), torch.float32, dev)
-    g = _block_grid(q_grid, k_grid, q_block, k_block)
-    with _op_device(dev, stream) as on:
+        _dense("lse", lse, (B, heads, p.Lq), torch.float32, dev)
+    with _on(dev, stream) as st:
         if out is None:
-            out = torch.empty((B, Lq, heads * 128), dtype=torch.bfloat16, device=dev)
-        ldo = _rows("out", out)
-        _tokens_match("out", out, B, q_grid, heads, dev)
-        ws = on.scratch(lib().wan_op_attention_blocks_workspace(B, heads, C.byref(g), topk), workspace)
-        _check(lib().wan_op_attention_blocks(_ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(out), ldo, B, heads, C.byref(g),
-                                             _ptr(blocks), _ptr(counts), topk, _ptr(lse), _ptr(ws), _nbytes(ws), on.stream),
-               "wan_op_attention_blocks")
+            out = torch.empty((B, p.Lq, D), dtype=torch.bfloat16, device=dev)
+            ldo = D
+        else:
+            ldo = _rows("out", out, B, p.Lq, D, dev)
+        if B == 0:
+            return out
+        ws, nbytes, _keep = _scratch(p.attend_bytes, workspace, dev)
+        _check(lib().wan_op_attention_blocks(q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, out.data_ptr(), ldo, B,
+                                             heads, p.ref, blocks.data_ptr(), counts.data_ptr(), topk, _ptr(lse), ws, nbytes,
+                                             st), "wan_op_attention_blocks")
     return out
 
 
-def _kv_cache(k_cache, v_cache, table, B) -> wan_kv_cache:
+def _kv_cache(k_cache, v_cache, table, B, D, device) -> wan_kv_cache:
     import torch
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if t.dim() != 3 or t.dtype != torch.bfloat16 or not t.is_cuda or t.stride(2) != 1:
-            raise ValueError(f"{name}: a CUDA bf16 tensor [pages, page size, D] with dense rows is needed, "
-                             f"got {tuple(t.shape)} {t.dtype}, strides {t.stride()}")
-    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride() or k_cache.device != v_cache.device:
-        raise ValueError("k_cache and v_cache must have one shape, one layout and one device")
-    if table.dim() != 2 or table.dtype != torch.int32 or table.stride(1) != 1 or table.shape[0] != B or \
-            table.device != k_cache.device:
-        raise ValueError(f"page table: an int32 tensor [{B}, pages] on {k_cache.device} is needed, "
-                         f"got {tuple(table.shape)} {table.dtype} on {table.device}")
-    return wan_kv_cache(k=k_cache.data_ptr(), v=v_cache.data_ptr(), page_stride=k_cache.stride(0),
-                        token_stride=k_cache.stride(1), num_pages=k_cache.shape[0], page_size=k_cache.shape[1],
-                        table=table.data_ptr(), table_ld=max(table.stride(0), table.shape[1]), max_pages=table.shape[1])
+    shape, st = k_cache.shape, k_cache.stride()
+    if k_cache.dtype is not torch.bfloat16 or v_cache.dtype is not torch.bfloat16 or len(shape) != 3 or shape[2] != D or \
+            st[2] != 1 or v_cache.shape != shape or v_cache.stride() != st or k_cache.device != device or \
+            v_cache.device != device or device.type != "cuda":
+        raise ValueError(f"k_cache, v_cache: bf16 tensors [pages, page size, {D}] of one layout with dense rows on {device} "
+                         f"are needed, got {tuple(shape)} and {tuple(v_cache.shape)}, strides {st} and {v_cache.stride()}")
+    ts, tst = table.shape, table.stride()
+    if len(ts) != 2 or table.dtype is not torch.int32 or (ts[1] > 1 and tst[1] != 1) or ts[0] != B or table.device != device:
+        raise ValueError(f"page table: an int32 tensor [{B}, pages] on {device} is needed, "
+                         f"got {tuple(ts)} {table.dtype} on {table.device}")
+    return wan_kv_cache(k_cache.data_ptr(), v_cache.data_ptr(), st[0] if shape[0] > 1 else shape[1] * st[1],
+                        st[1] if shape[1] > 1 else D, shape[0], shape[1], table.data_ptr(),
+                        tst[0] if B > 1 else ts[1], ts[1])
 
 
 def op_kv_append(k, v, k_cache, v_cache, table, start, heads, frame, count=None, k_gain=None, q=None, q_gain=None,
@@ -643,36 +664,40 @@ def op_kv_append(k, v, k_cache, v_cache, table, start, heads, frame, count=None,
     the token grid, gains f32 [D] (None: no norm).  Returns the rotated queries (q_out, by default a new tensor
     with zero rows past count) or None without q."""
     import torch
-    B, T, dev, D = k.shape[0], k.shape[1], k.device, heads * 128
-    ldk, ldv = _rows("k", k), _rows("v", v)
-    for name, t in (("k", k), ("v", v), ("q", q), ("q_out", q_out)):
-        if t is not None and (tuple(t.shape) != (B, T, D) or t.device != dev):
-            raise ValueError(f"{name}: [{B}, {T}, {D}] on {dev} is needed, got {tuple(t.shape)} on {t.device}")
+    B, T = k.shape[:2]
+    dev, D = k.device, heads * 128
+    ldk, ldv = _rows("k", k, B, T, D, dev), _rows("v", v, B, T, D, dev)
     _dense("start", start, (B,), torch.int32, dev)
     if count is not None:
         _dense("count", count, (B,), torch.int32, dev)
-    for name, t in (("k_gain", k_gain), ("q_gain", q_gain)):
-        if t is not None:
-            _dense(name, t, (D,), torch.float32, dev)
-    c = _kv_cache(k_cache, v_cache, table, B)
-    if k_cache.device != dev or k_cache.shape[2] != D:
-        raise ValueError(f"k_cache: rows of {D} on {dev} are needed, got {tuple(k_cache.shape)} on {k_cache.device}")
-    with _op_device(dev, stream) as on:
-        ldq = ldqo = 0
-        if q is not None:
+    if k_gain is not None:
+        _dense("k_gain", k_gain, (D,), torch.float32, dev)
+    if q_gain is not None:
+        _dense("q_gain", q_gain, (D,), torch.float32, dev)
+    c = _kv_cache(k_cache, v_cache, table, B, D, dev)
+    ldq = ldqo = 0
+    with _on(dev, stream) as st:
+        if q is None:
+            q_out = None
+        else:
+            ldq = _rows("q", q, B, T, D, dev)
             if q_out is None:
-                q_out = torch.empty((B, T, D), dtype=torch.bfloat16, device=dev) if count is None else \
-                    torch.zeros((B, T, D), dtype=torch.bfloat16, device=dev)
-            ldq, ldqo = _rows("q", q), _rows("q_out", q_out)
-        _check(lib().wan_op_kv_append(_ptr(k), ldk, _ptr(v), ldv, B, T, heads, _ptr(start), _ptr(count), _ptr(k_gain), eps,
-                                      int(rope), frame[0], frame[1], split[0], split[1], split[2], theta, _ptr(q), ldq,
-                                      _ptr(q_gain), _ptr(q_out) if q is not None else None, ldqo, C.byref(c), on.stream),
+                q_out = (torch.empty if count is None else torch.zeros)((B, T, D), dtype=torch.bfloat16, device=dev)
+                ldqo = D
+            else:
+                ldqo = _rows("q_out", q_out, B, T, D, dev)
+        if B == 0 or T == 0:
+            return q_out
+        _check(lib().wan_op_kv_append(k.data_ptr(), ldk, v.data_ptr(), ldv, B, T, heads, start.data_ptr(), _ptr(count),
+                                      _ptr(k_gain), eps, 1 if rope else 0, frame[0], frame[1], split[0], split[1], split[2],
+                                      theta, _ptr(q), ldq, _ptr(q_gain), _ptr(q_out), ldqo, C.byref(c), st),
                "wan_op_kv_append")
-    return q_out if q is not None else None
+    return q_out
 
 
 def op_attention_paged_workspace(B, heads, T, k_cache, v_cache, table) -> int:
-    return lib().wan_op_attention_paged_workspace(B, heads, T, C.byref(_kv_cache(k_cache, v_cache, table, B)))
+    c = _kv_cache(k_cache, v_cache, table, B, heads * 128, k_cache.device)
+    return lib().wan_op_attention_paged_workspace(B, heads, T, C.byref(c))
 
 
 def op_attention_paged(q, k_cache, v_cache, table, lens, heads, out=None, lse=None, workspace=None, stream=None):
@@ -680,24 +705,25 @@ def op_attention_paged(q, k_cache, v_cache, table, lens, heads, out=None, lse=No
     [B, T, D], caches bf16 [pages, page size, D], table int32 [B, pages], lens int32 [B]; lse f32 [B, heads, T] is
     filled if given.  Returns out, bf16 [B, T, D]."""
     import torch
-    B, T, dev = q.shape[0], q.shape[1], q.device
-    ldq = _rows("q", q)
-    c = _kv_cache(k_cache, v_cache, table, B)
-    if q.shape[2] != heads * 128 or k_cache.shape[2] != heads * 128 or k_cache.device != dev:
-        raise ValueError(f"q and the caches need rows of {heads * 128} on one device, got {tuple(q.shape)} on {dev} and "
-                         f"{tuple(k_cache.shape)} on {k_cache.device}")
+    B, T = q.shape[:2]
+    dev, D = q.device, heads * 128
+    ldq = _rows("q", q, B, T, D, dev)
+    c = _kv_cache(k_cache, v_cache, table, B, D, dev)
     _dense("lens", lens, (B,), torch.int32, dev)
     if lse is not None:
         _dense("lse", lse, (B, heads, T), torch.float32, dev)
-    with _op_device(dev, stream) as on:
+    with _on(dev, stream) as st:
         if out is None:
-            out = torch.empty((B, T, heads * 128), dtype=torch.bfloat16, device=dev)
-        ldo = _rows("out", out)
-        if tuple(out.shape) != tuple(q.shape) or out.device != dev:
-            raise ValueError(f"out: {tuple(q.shape)} on {dev} is needed, got {tuple(out.shape)} on {out.device}")
-        ws = on.scratch(lib().wan_op_attention_paged_workspace(B, heads, T, C.byref(c)), workspace)
-        _check(lib().wan_op_attention_paged(_ptr(q), ldq, C.byref(c), _ptr(lens), _ptr(out), ldo, B, heads, T, _ptr(lse),
-                                            _ptr(ws), _nbytes(ws), on.stream), "wan_op_attention_paged")
+            out = torch.empty((B, T, D), dtype=torch.bfloat16, device=dev)
+            ldo = D
+        else:
+            ldo = _rows("out", out, B, T, D, dev)
+        if B == 0 or T == 0:
+            return out
+        need = _paged_bytes(B, heads, T, c.page_stride, c.token_stride, c.num_pages, c.page_size, c.table_ld, c.max_pages)
+        ws, nbytes, _keep = _scratch(need, workspace, dev)
+        _check(lib().wan_op_attention_paged(q.data_ptr(), ldq, C.byref(c), lens.data_ptr(), out.data_ptr(), ldo, B, heads, T,
+                                            _ptr(lse), ws, nbytes, st), "wan_op_attention_paged")
     return out
 
 

@@ -4,12 +4,16 @@
 // page that holds the place; the value row is copied; query rows get the same
 // norm and rotation into a buffer of their own.
 //
-// Memory bound: each row is read once and written once.  One warp per row; a
-// lane's 16-byte vectors are lane, lane + 32, ..., and since a head is 16
-// vectors all of them sit at the same place of their head, so a lane needs four
-// (cos, sin) pairs in all and computes them itself: the angle and its remainder
-// by 2 pi in fp64 (a position of 1e5 leaves no fraction bits of the angle in
-// fp32), cos and sin of the remainder in fp32.
+// Memory bound: each row is read once and written once, through registers, by 1, 2,
+// 4 or 8 warps (up to 6 vectors of 16 bytes per lane, loaded before anything is
+// looked up).  Many short warps hide the chain from the sequence's first place over
+// its page to the store; groups that took several rows each, the next row's loads in
+// flight and the gains in registers, had a third of the warps and took 1.3 times
+// the time.  A lane's vectors lie 32 apart and a head is 16 vectors, so all of them sit at the
+// same place of their head: a lane needs four (cos, sin) pairs, computes two and
+// gets the others from the lane 16 further.  The angle is taken in turns in fp64,
+// its whole turns dropped, and only the remainder goes to fp32 (a position of 1e5
+// leaves no fraction bits of the angle there).
 #include "common.cuh"
 #include "kernels.h"
 
@@ -28,7 +32,8 @@ struct AppendParams {
     int rope, H, W;
     int nt, nh;             // pairs of the frame and row axes
     KvPages c;
-    double freq[64];        // theta^(-2 p / width) of pair p in its axis
+    int log_page;
+    double turns[64];       // theta^(-2 p / width) / (2 pi) of pair p in its axis
 };
 
 __device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
@@ -41,48 +46,43 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
     }
 }
 
-// grid: rows / 8 x {k, v[, q]}
-__global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ AppendParams p) {
-    const int lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (row >= (long long)p.B * p.T) return;
-    const int b = (int)(row / p.T), t = (int)(row % p.T);
-    if (p.count && t >= __ldg(p.count + b)) return;
-    const int first = __ldg(p.start + b);
-    const long long slot = (long long)first + t;
+// grid: groups of rows x {k, v[, q]}; heads * 16 <= 32 NV WPR
+template <int NV, int WPR>
+__global__ void __launch_bounds__(256, 4) kv_append_kernel(const __grid_constant__ AppendParams p) {
+    __shared__ float sums[8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int sub = warp % WPR, group = warp / WPR;
     const int what = blockIdx.y;  // 0 k, 1 v, 2 q
     const int vecs = p.heads * 16;
-    const __nv_bfloat16* src = what == 0 ? p.k + row * p.ldk : what == 1 ? p.v + row * p.ldv : p.q + row * p.ldq;
-    __nv_bfloat16* dst;
+    const long long row = (long long)blockIdx.x * (8 / WPR) + group;
+    if (row >= (long long)p.B * p.T) return;
+    const int b = (int)(row / p.T), t = (int)(row - (long long)b * p.T);
+    const int first = __ldg(p.start + b);
+    if (p.count && t >= __ldg(p.count + b)) return;
+    const uint4* src = reinterpret_cast<const uint4*>(what == 0 ? p.k + row * p.ldk : what == 1 ? p.v + row * p.ldv
+                                                                                                : p.q + row * p.ldq);
+    auto vec = [&](int i) { return (i * WPR + sub) * 32 + lane; };
+    uint4 x[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) x[i] = vec(i) < vecs ? src[vec(i)] : make_uint4(0, 0, 0, 0);
+    if (first < 0) return;
+    const uint32_t slot = (uint32_t)first + (uint32_t)t;
+    uint4* dst;
     if (what == 2) {
-        if (first < 0) return;
-        dst = p.q_out + row * p.ldqo;
+        dst = reinterpret_cast<uint4*>(p.q_out + row * p.ldqo);
     } else {
-        const long long at = slot / p.c.page_size;
-        if (first < 0 || at >= p.c.max_pages) return;
+        const uint32_t at = slot >> p.log_page;
+        if (at >= (uint32_t)p.c.max_pages) return;
         const int page = __ldg(p.c.table + (long long)b * p.c.table_ld + at);
         if (page < 0 || page >= p.c.num_pages) return;
-        dst = reinterpret_cast<__nv_bfloat16*>(what == 0 ? p.c.k : p.c.v) + page * p.c.page_stride +
-              (slot - at * p.c.page_size) * p.c.token_stride;
+        dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(what == 0 ? p.c.k : p.c.v) + page * p.c.page_stride +
+                                       (long long)(slot & ((1u << p.log_page) - 1)) * p.c.token_stride);
     }
     if (what == 1) {
-        for (int i = lane; i < vecs; i += 32)
-            reinterpret_cast<uint4*>(dst)[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (vec(i) < vecs) dst[vec(i)] = x[i];
         return;
-    }
-    const float* gain = what == 0 ? p.k_gain : p.q_gain;
-    float scale = 1.0f;
-    if (gain) {
-        float ss = 0.f;
-        for (int i = lane; i < vecs; i += 32) {
-            float x[8];
-            unpack8(reinterpret_cast<const uint4*>(src)[i], x);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) ss += x[c] * x[c];
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        scale = rsqrtf(ss / (float)(p.heads * 128) + p.eps);
     }
     float cs[4], sn[4];
 #pragma unroll
@@ -91,34 +91,72 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ 
         sn[i] = 0.f;
     }
     if (p.rope) {
-        const long long hw = (long long)p.H * p.W;
-        const long long f = slot / hw;
-        const int in = (int)(slot - f * hw), ih = in / p.W, iw = in - ih * p.W;
+        const uint32_t hw = (uint32_t)p.H * (uint32_t)p.W;
+        const uint32_t f = slot / hw, in = slot - f * hw, ih = in / (uint32_t)p.W, iw = in - ih * (uint32_t)p.W;
+        const bool upper = lane >= 16;  // this half's two pairs: 0, 1 or 2, 3
+        float c2[2], s2[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int pair = (lane & 15) * 4 + i;
-            const double pos = pair < p.nt ? (double)f : pair < p.nt + p.nh ? (double)ih : (double)iw;
-            const double angle = pos * p.freq[pair];
-            const double turns = rint(angle * 0.15915494309189535);  // 1 / (2 pi)
-            sincosf((float)fma(turns, -6.283185307179586, angle), &sn[i], &cs[i]);
+        for (int i = 0; i < 2; ++i) {
+            const int pair = (lane & 15) * 4 + (upper ? 2 : 0) + i;
+            const uint32_t pos = pair < p.nt ? f : pair < p.nt + p.nh ? ih : iw;
+            const double turns = (double)pos * p.turns[pair];
+            sincospif(2.0f * (float)(turns - rint(turns)), &s2[i], &c2[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float oc = __shfl_xor_sync(0xffffffffu, c2[i], 16), os = __shfl_xor_sync(0xffffffffu, s2[i], 16);
+            cs[i] = upper ? oc : c2[i];
+            sn[i] = upper ? os : s2[i];
+            cs[i + 2] = upper ? c2[i] : oc;
+            sn[i + 2] = upper ? s2[i] : os;
         }
     }
-    for (int i = lane; i < vecs; i += 32) {
-        float x[8];
-        unpack8(reinterpret_cast<const uint4*>(src)[i], x);
+    const float* gain = what == 0 ? p.k_gain : p.q_gain;
+    float scale = 1.0f;
+    if (gain) {
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float y[8];
+            unpack8(x[i], y);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) ss += y[c] * y[c];
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (WPR > 1) {  // the row's other warps (the same row, so the same path)
+            if (lane == 0) sums[warp] = ss;
+            named_bar(1 + group, WPR * 32);
+            ss = 0.f;
+#pragma unroll
+            for (int w = 0; w < WPR; ++w) ss += sums[group * WPR + w];
+        }
+        scale = rsqrtf(ss / (float)(p.heads * 128) + p.eps);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (vec(i) >= vecs) continue;
+        float y[8];
+        unpack8(x[i], y);
         if (gain) {
-            const float4 g0 = __ldg(reinterpret_cast<const float4*>(gain) + 2 * i);
-            const float4 g1 = __ldg(reinterpret_cast<const float4*>(gain) + 2 * i + 1);
+            const float4 g0 = __ldg(reinterpret_cast<const float4*>(gain) + 2 * vec(i));
+            const float4 g1 = __ldg(reinterpret_cast<const float4*>(gain) + 2 * vec(i) + 1);
             const float g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
 #pragma unroll
-            for (int c = 0; c < 8; ++c) x[c] = x[c] * scale * g[c];
+            for (int c = 0; c < 8; ++c) y[c] = y[c] * scale * g[c];
         }
         uint32_t o[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-            o[c] = pack_bf16(x[2 * c] * cs[c] - x[2 * c + 1] * sn[c], x[2 * c] * sn[c] + x[2 * c + 1] * cs[c]);
-        reinterpret_cast<uint4*>(dst)[i] = make_uint4(o[0], o[1], o[2], o[3]);
+        for (int c = 0; c < 4; ++c)  // the one rounding to bf16
+            o[c] = pack_bf16(y[2 * c] * cs[c] - y[2 * c + 1] * sn[c], y[2 * c] * sn[c] + y[2 * c + 1] * cs[c]);
+        dst[vec(i)] = make_uint4(o[0], o[1], o[2], o[3]);
     }
+}
+
+template <int NV, int WPR>
+void append(const AppendParams& p, cudaStream_t stream) {
+    const long long rows = (long long)p.B * p.T, per = 8 / WPR;
+    kv_append_kernel<NV, WPR><<<dim3((unsigned)((rows + per - 1) / per), p.q ? 3 : 2), 256, 0, stream>>>(p);
 }
 
 }  // namespace
@@ -150,13 +188,20 @@ cudaError_t launch_kv_append(const void* k, long long ldk, const void* v, long l
     p.nt = rope_t / 2;
     p.nh = rope_h / 2;
     p.c = c;
+    while ((1 << p.log_page) < c.page_size) ++p.log_page;
     if (rope) {
         const int width[3] = {rope_t, rope_h, rope_w};
         for (int a = 0, n = 0; a < 3; ++a)
-            for (int i = 0; i < width[a] / 2; ++i) p.freq[n++] = pow(theta, -2.0 * i / width[a]);
+            for (int i = 0; i < width[a] / 2; ++i) p.turns[n++] = pow(theta, -2.0 * i / width[a]) * 0.15915494309189533577;
     }
-    const dim3 grid((unsigned)(((long long)B * T + 7) / 8), q ? 3 : 2);
-    kv_append_kernel<<<grid, 256, 0, ctx.stream>>>(p);
+    const int nv = (heads * 16 + 31) / 32;  // vectors per lane of one warp
+    if (nv <= 1) append<1, 1>(p, ctx.stream);
+    else if (nv <= 3) append<3, 1>(p, ctx.stream);
+    else if (nv <= 6) append<6, 1>(p, ctx.stream);
+    else if (nv <= 12) append<6, 2>(p, ctx.stream);
+    else if (nv <= 20) append<5, 4>(p, ctx.stream);
+    else if (nv <= 48) append<6, 8>(p, ctx.stream);
+    else return cudaErrorInvalidValue;
     if (ctx.launches) ++*ctx.launches;
     return cudaGetLastError();
 }
