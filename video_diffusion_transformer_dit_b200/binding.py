@@ -539,23 +539,31 @@ def _paged_bytes(B, heads, T, page_stride, token_stride, num_pages, page_size, t
     return lib().wan_op_attention_paged_workspace(B, heads, T, C.byref(c))
 
 
+def _current_raw_stream(index: int) -> int:
+    """Handle of the device's current stream (torch's own short way to it where there is one)."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
+
+
 class _on:
     """The tensors' device and the launch stream made current for a call: buffers that the call allocates
     belong to the stream that uses them.  Gives the stream's handle."""
+    __slots__ = ("device", "enter")
 
     def __init__(self, device, stream):
         import torch
-        self.enter = []
-        if device.index != torch.cuda.current_device():
-            self.enter.append(torch.cuda.device(device))
-        if stream is not None:
-            s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
-            self.enter.append(torch.cuda.stream(s))
+        self.device, self.enter = device, ()
+        if stream is not None or device.index != torch.cuda.current_device():
+            self.enter = [torch.cuda.device(device)]
+            if stream is not None:
+                s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+                self.enter.append(torch.cuda.stream(s))
 
     def __enter__(self):
         for c in self.enter:
             c.__enter__()
-        return _stream()
+        return _current_raw_stream(self.device.index)
 
     def __exit__(self, *exc):
         for c in reversed(self.enter):

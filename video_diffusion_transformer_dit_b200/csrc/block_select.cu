@@ -40,8 +40,10 @@ constexpr float SCORE_ERROR = 1.007e-3f;
 constexpr float SCORE_TINY = 1e-36f;            // below it scores lose bits to underflow
 
 // Means of the blocks of q (first g.q_blocks() CTAs) and k, per head: fp64, fp16 of
-// unit length, and norm (NaN or infinite where a mean is).  One CTA per block and 256-thread column slice,
-// eight columns per thread; four tokens are added in fp32 before they join the
+// unit length, and norm (NaN or infinite where a mean is).  One CTA per block and
+// column slice, eight columns per thread; where there are few of them (a small
+// grid) RG = 4 groups of threads take every fourth eight tokens each: a block is a
+// chain of loads, 14 -> 9 us at 15 blocks; four tokens are added in fp32 before they join the
 // fp64 sum: bf16 has 8 significant bits, so a sum of four of them is exact in
 // fp32's 24 unless their exponents lie 14 apart.
 struct MeanOut {
@@ -49,6 +51,7 @@ struct MeanOut {
     __half* unit;           // [B, heads, blocks, 128], null: not wanted
     float* norm;            // [B, heads, blocks]
 };
+template <int RG>
 __global__ void __launch_bounds__(256) block_mean_kernel(const __nv_bfloat16* __restrict__ q, long long ldq,
                                                          const __nv_bfloat16* __restrict__ k, long long ldk, int heads,
                                                          const __grid_constant__ BlockGrid g, const MeanOut oq,
@@ -64,7 +67,7 @@ __global__ void __launch_bounds__(256) block_mean_kernel(const __nv_bfloat16* __
     const int f0 = blk / (nH * nW) * box[0], i0 = blk / nW % nH * box[1], j0 = blk % nW * box[2];
     const int ef = min(box[0], F - f0), ei = min(box[1], H - i0), ej = min(box[2], W - j0);
     const int n = ef * ei * ej;
-    for (int t = threadIdx.x; t < n; t += blockDim.x)
+    for (int t = threadIdx.y * blockDim.x + threadIdx.x; t < n; t += RG * blockDim.x)
         tokens[t] = ((f0 + t / (ej * ei)) * H + i0 + t / ej % ei) * W + j0 + t % ej;
     __syncthreads();
     const int col = (blockIdx.y * blockDim.x + threadIdx.x) * 8;
@@ -89,20 +92,33 @@ __global__ void __launch_bounds__(256) block_mean_kernel(const __nv_bfloat16* __
 #pragma unroll
         for (int c = 0; c < 8; ++c) acc[c] += (double)s[c];
     };
-    int t = 0;
-    for (; t + 8 <= n; t += 8) {
+    int t = threadIdx.y * 8;
+    for (; t + 8 <= n; t += 8 * RG) {
         uint4 v[2][4];
 #pragma unroll
         for (int u = 0; u < 8; ++u) v[u >> 2][u & 3] = __ldg(reinterpret_cast<const uint4*>(base + (long long)tokens[t + u] * ld));
         add(v[0]);
         add(v[1]);
     }
-    for (; t < n; t += 4) {
+    for (const int last = min(n, t + 8); t < last; t += 4) {  // one group at most comes to a rest
         uint4 v[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u)
             v[u] = t + u < n ? __ldg(reinterpret_cast<const uint4*>(base + (long long)tokens[t + u] * ld)) : make_uint4(0, 0, 0, 0);
         add(v);
+    }
+    if constexpr (RG > 1) {
+        __shared__ double part[RG - 1][8][64];
+        if (threadIdx.y > 0) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) part[threadIdx.y - 1][c][threadIdx.x] = acc[c];
+        }
+        __syncthreads();
+        if (threadIdx.y > 0) return;
+#pragma unroll
+        for (int r = 0; r < RG - 1; ++r)
+#pragma unroll
+            for (int c = 0; c < 8; ++c) acc[c] += part[r][c][threadIdx.x];
     }
     const MeanOut& o = keys ? ok : oq;
     const long long at = ((long long)b * heads + (mine ? col / 128 : 0)) * (nF * nH * nW) + blk;
@@ -706,10 +722,13 @@ cudaError_t launch_block_select(const void* q, long long ldq, const void* k, lon
         ok.norm = oq.norm + bh * nq;
     }
     const int vecs = heads * 16;
-    const int threads = vecs < 256 ? (vecs + 31) / 32 * 32 : 256;
-    const int slices = (vecs + threads - 1) / threads;
-    block_mean_kernel<<<dim3(nq + nk, slices, B), threads, 0, ctx.stream>>>(
-        reinterpret_cast<const __nv_bfloat16*>(q), ldq, reinterpret_cast<const __nv_bfloat16*>(k), ldk, heads, g, oq, ok);
+    auto mean = [&](auto kernel, int most, int groups) {
+        const int threads = vecs < most ? (vecs + 31) / 32 * 32 : most;
+        kernel<<<dim3(nq + nk, (vecs + threads - 1) / threads, B), dim3(threads, groups), 0, ctx.stream>>>(
+            reinterpret_cast<const __nv_bfloat16*>(q), ldq, reinterpret_cast<const __nv_bfloat16*>(k), ldk, heads, g, oq, ok);
+    };
+    if ((long long)(nq + nk) * vecs * B < 148 * 1024) mean(block_mean_kernel<4>, 64, 4);
+    else mean(block_mean_kernel<1>, 256, 1);
     if (fast) {
         block_score_kernel<<<dim3((nk + ST - 1) / ST, (nq + ST - 1) / ST, (unsigned)bh), 128, 0, ctx.stream>>>(
             oq.unit, ok.unit, ok.norm, nq, nk, pitch, scores);
