@@ -310,6 +310,8 @@ __global__ void __launch_bounds__(alist::THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+    // every CTA is resident: the join may take the SMs that are done, and wait
+    if (p.splits > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // producer: slots with a load issued and the phase it completes, phase of the
     // last Q load; issuer: whether any MMA went out (both drained after an abort)
     uint32_t armed = 0, par = 0;
@@ -739,17 +741,17 @@ __global__ void __launch_bounds__(alist::THREADS, 1)
 }
 
 // Joins the parts of one query row's list: O = sum_s w_s O_s, w_s = 2^(lse_s -
-// lse).  One warp per row; a part without keys has lse -inf and is not read.
+// lse); a part without keys has lse -inf and is not read.  A CTA takes JOIN_ROWS
+// rows of one query tile, two per warp: it is latency that bounds it (the first
+// 32 parts' lse of both rows in one round, then eight parts' rows at a time).  It is
+// launched while the attention kernel still runs and waits for it after its set-up.
+constexpr int JOIN_ROWS = 16;
 template <alist::Mode MODE>
 __global__ void __launch_bounds__(256) list_join_kernel(const __grid_constant__ ListParams p) {
-    const int lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per = p.nqb * p.heads * p.B;
-    if (row >= (long long)per * p.rows) return;
-    const int unit = (int)(row / p.rows), r = (int)(row % p.rows);
+    const int unit = blockIdx.x;
     const int qt = unit % p.nqb, h = unit / p.nqb % p.heads, b = unit / p.nqb / p.heads;
-    const int token = list_token<MODE>(p, qt, r);
-    if (token < 0) return;
     const int Lq = MODE == alist::BLOCKS ? p.g.q_tokens() : p.T;
     int s0 = 0, s1 = p.splits - 1;
     bool inside = false;  // pages: the first part begins inside its range
@@ -775,46 +777,62 @@ __global__ void __launch_bounds__(256) list_join_kernel(const __grid_constant__ 
         if (s0 == s1) return;  // whole in one range: written by its unit
         inside = (uint32_t)((unsigned long long)total * s0 / ranges) < first;
     }
-    auto at = [&](int s) {
-        if (MODE == alist::BLOCKS) return ((long long)s * per + unit) * p.rows + r;
+    auto part = [&](int s) -> long long {
+        if (MODE == alist::BLOCKS) return (long long)s * per + unit;
         const long long u = (long long)s * (p.nqb * p.heads) + h * p.nqb + qt;
-        return (u * 2 + (s == s0 && inside)) * p.rows + r;
+        return u * 2 + (s == s0 && inside);
     };
-    // a lane per part for its lse, then all lanes add up the parts' rows, a few loads in flight
-    float m = -INFINITY;
-    for (int s = s0 + lane; s <= s1; s += 32) m = fmaxf(m, p.part_lse[at(s)]);
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written
+    int token[2];
+    float l[2];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float total = 0.f;
-    for (int c = s0; c <= s1; c += 32) {
-        const float l = c + lane <= s1 ? p.part_lse[at(c + lane)] : -INFINITY;
-        const float w = l == -INFINITY ? 0.0f : exp2f(l - m);
-        const int n = min(32, s1 - c + 1);
-        for (int i = 0; i < n; i += 8) {
-            float4 x[8];
-            float wi[8];
+    for (int i = 0; i < 2; ++i) {
+        const int r = blockIdx.y * JOIN_ROWS + warp * 2 + i;
+        token[i] = r < p.rows ? list_token<MODE>(p, qt, r) : -1;
+        l[i] = token[i] >= 0 && s0 + lane <= s1 ? p.part_lse[part(s0 + lane) * p.rows + r] : -INFINITY;
+    }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                wi[j] = i + j < n ? __shfl_sync(0xffffffffu, w, (i + j) & 31) : 0.0f;
-                x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (wi[j] != 0.0f) x[j] = *reinterpret_cast<const float4*>(p.part_o + at(c + i + j) * 128 + lane * 4);
-            }
+    for (int i = 0; i < 2; ++i) {
+        if (token[i] < 0) continue;
+        const int r = blockIdx.y * JOIN_ROWS + warp * 2 + i;
+        // a lane per part for its lse, then all lanes add up the parts' rows
+        float m = l[i];
+        for (int s = s0 + lane + 32; s <= s1; s += 32) m = fmaxf(m, p.part_lse[part(s) * p.rows + r]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                total += wi[j];
-                acc.x += wi[j] * x[j].x;
-                acc.y += wi[j] * x[j].y;
-                acc.z += wi[j] * x[j].z;
-                acc.w += wi[j] * x[j].w;
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float total = 0.f;
+        for (int c = s0; c <= s1; c += 32) {
+            const float lc = c == s0 ? l[i] : c + lane <= s1 ? p.part_lse[part(c + lane) * p.rows + r] : -INFINITY;
+            const float w = lc == -INFINITY ? 0.0f : exp2f(lc - m);
+            const int n = min(32, s1 - c + 1);
+            for (int k = 0; k < n; k += 8) {
+                float4 x[8];
+                float wk[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    wk[j] = k + j < n ? __shfl_sync(0xffffffffu, w, (k + j) & 31) : 0.0f;
+                    x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (wk[j] != 0.0f)
+                        x[j] = *reinterpret_cast<const float4*>(p.part_o + (part(c + k + j) * p.rows + r) * 128 + lane * 4);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    total += wk[j];
+                    acc.x += wk[j] * x[j].x;
+                    acc.y += wk[j] * x[j].y;
+                    acc.z += wk[j] * x[j].z;
+                    acc.w += wk[j] * x[j].w;
+                }
             }
         }
+        const float inv = total == 0.f ? 0.f : 1.0f / total;
+        uint2 out = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+        *reinterpret_cast<uint2*>(p.o + ((long long)b * Lq + token[i]) * p.ldo + h * 128 + lane * 4) = out;
+        if (p.lse && lane == 0)
+            p.lse[((long long)b * p.heads + h) * Lq + token[i]] =
+                total == 0.f ? -INFINITY : (m + log2f(total)) * 0.6931471805599453f;
     }
-    const float inv = total == 0.f ? 0.f : 1.0f / total;
-    uint2 out = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-    *reinterpret_cast<uint2*>(p.o + ((long long)b * Lq + token) * p.ldo + h * 128 + lane * 4) = out;
-    if (p.lse && lane == 0)
-        p.lse[((long long)b * p.heads + h) * Lq + token] = total == 0.f ? -INFINITY : (m + log2f(total)) * 0.6931471805599453f;
 }
 
 cudaError_t init_attention_list_attributes() {
@@ -867,7 +885,17 @@ cudaError_t launch_list(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
     attn_list_kernel<MODE><<<ctas < ctx.num_sms ? ctas : ctx.num_sms, alist::THREADS, alist::SMEM_BYTES, ctx.stream>>>(tq, tk, tv, p);
     if (ctx.launches) ++*ctx.launches;
     if (p.splits > 1) {
-        list_join_kernel<MODE><<<(unsigned)((per * p.rows + 7) / 8), 256, 0, ctx.stream>>>(p);
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)per, (p.rows + JOIN_ROWS - 1) / JOIN_ROWS);
+        cfg.blockDim = dim3(256);
+        cfg.stream = ctx.stream;
+        cudaLaunchAttribute early{};
+        early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        early.val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = &early;
+        cfg.numAttrs = 1;
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, list_join_kernel<MODE>, static_cast<const ListParams&>(p));
+        if (e != cudaSuccess) return e;
         if (ctx.launches) ++*ctx.launches;
     }
     return cudaGetLastError();
