@@ -195,9 +195,10 @@ typedef struct {
  * split and pairs as wan_op_rmsnorm_rope), rounded once and stored; the value
  * row is copied.  With q != NULL the query rows get q_gain's norm and the same
  * rotation into q_out (may be q itself).  Rows t >= count[b], places past the
- * table (start[b] < 0 too) and pages that are not there are left as they were
- * (q_out is written for every t < count[b] with start[b] >= 0).  Two sequences
- * that share a page must not write the same place.
+ * table (start[b] < 0 too) and pages that are not there are left as they were;
+ * q_out is written for every t < count[b] with start[b] >= 0, and its other rows
+ * are zeroed if zero_rest != 0 (for a buffer that is not q itself) or left.  Two
+ * sequences that share a page must not write the same place.
  * Errors before any launch: WAN_EINVAL for a null pointer, WAN_ESHAPE for B, T <
  * 0, heads outside [1, 96], a RoPE split that is not even with sum 128, H, W <= 0, theta <=
  * 0, strides or pointers (k, v, q, q_out, the cache, gains) that are not
@@ -207,7 +208,7 @@ WANDIT_API wan_status wan_op_kv_append(const void* k, int64_t ldk, const void* v
                                        const int32_t* start, const int32_t* count, const float* k_gain, float eps,
                                        int rope, int H, int W, int rope_t, int rope_h, int rope_w, float theta,
                                        const void* q, int64_t ldq, const float* q_gain, void* q_out, int64_t ldqo,
-                                       const wan_kv_cache* cache, void* stream);
+                                       int zero_rest, const wan_kv_cache* cache, void* stream);
 
 /* Attention of T >= 1 new tokens per sequence over its cache: O = softmax(Q K^T /
  * sqrt(128)) V over places [0, lens[b]) (lens[b] is held to [0, max_pages *

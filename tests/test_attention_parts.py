@@ -102,7 +102,7 @@ def test_kv_append_refuses(lib):
         c = a["c"]
         return lib.wan_op_kv_append(a["k"], a["ldk"], a["v"], a["ldv"], a["B"], a["T"], a["heads"], a["start"], a["count"],
                                     a["k_gain"], 1e-6, a["rope"], a["H"], a["W"], *a["split"], a["theta"], a["q"], a["ldq"],
-                                    a["q_gain"], a["q_out"], a["ldqo"], C.byref(c) if c else None, None)
+                                    a["q_gain"], a["q_out"], a["ldqo"], 0, C.byref(c) if c else None, None)
 
     for kw in (dict(k=None), dict(v=None), dict(start=None), dict(c=None), dict(q_out=None), dict(c=cache(k=None)),
                dict(c=cache(v=None)), dict(c=cache(table=None))):

@@ -584,3 +584,17 @@ def test_block_select_on_both_sides_of_the_two_stage_limit(nk):
     B().op_sync()
     want = R.select(q, k, *args)
     assert torch.equal(blocks.cpu(), want[0]) and torch.equal(counts.cpu(), want[1])
+
+
+def test_kv_append_zeroes_the_rest_of_a_new_query_buffer():
+    heads, page, T = 17, 32, 11
+    kc, vc, table = cache(3, 2, page, heads, 121)
+    q, k, v = packed(3, T, heads, 122)
+    start = torch.tensor([0, 5, -2], dtype=torch.int32, device="cuda")
+    count = torch.tensor([4, 0, 11], dtype=torch.int32, device="cuda")
+    torch.full((3, T, heads * 128), math.nan, dtype=torch.bfloat16, device="cuda")      # memory the new buffer may take
+    q_out = B().op_kv_append(k, v, kc, vc, table, start, heads, (3, 4), count=count, q=q)
+    B().op_sync()
+    assert bool((q_out[0, 4:] == 0).all()) and bool((q_out[1:] == 0).all())
+    y, size = R.rotated(q[0, :4].to(DT), torch.arange(4, device="cuda"), heads, (3, 4), None)
+    assert bool(((q_out[0, :4].to(DT) - y).abs() <= R.HALF_STEP * 1.001 * y.abs() + 2.0 ** -20 * size).all())

@@ -147,7 +147,7 @@ def lib() -> C.CDLL:
                                         I64, P]),
         "wan_op_attention_blocks_workspace": (I64, [I, I, C.POINTER(wan_block_grid), I]),
         "wan_op_kv_append": (I, [P, I64, P, I64, I, I, I, P, P, P, F, I, I, I, I, I, I, F, P, I64, P, P, I64,
-                                 C.POINTER(wan_kv_cache), P]),
+                                 I, C.POINTER(wan_kv_cache), P]),
         "wan_op_attention_paged": (I, [P, I64, C.POINTER(wan_kv_cache), P, P, I64, I, I, I, P, P, I64, P]),
         "wan_op_attention_paged_workspace": (I64, [I, I, I, C.POINTER(wan_kv_cache)]),
         "wan_op_conv3d": (I, [P, P, I, I, I, I, I, I, P, I64, P, I, I, I, I, I, P, I64, P, I64, I, P]),
@@ -670,7 +670,7 @@ def op_kv_append(k, v, k_cache, v_cache, table, start, heads, frame, count=None,
     """Append T new tokens per sequence to a paged cache (wan_op_kv_append): k, v (and q) bf16 [B, T, D], caches
     bf16 [pages, page size, D], table int32 [B, pages], start (and count) int32 [B], frame = (rows, columns) of
     the token grid, gains f32 [D] (None: no norm).  Returns the rotated queries (q_out, by default a new tensor
-    with zero rows past count) or None without q."""
+    whose rows past count are zero) or None without q."""
     import torch
     B, T = k.shape[:2]
     dev, D = k.device, heads * 128
@@ -683,22 +683,21 @@ def op_kv_append(k, v, k_cache, v_cache, table, start, heads, frame, count=None,
     if q_gain is not None:
         _dense("q_gain", q_gain, (D,), torch.float32, dev)
     c = _kv_cache(k_cache, v_cache, table, B, D, dev)
-    ldq = ldqo = 0
+    ldq = ldqo = fresh = 0
     with _on(dev, stream) as st:
         if q is None:
             q_out = None
         else:
             ldq = _rows("q", q, B, T, D, dev)
             if q_out is None:
-                q_out = (torch.empty if count is None else torch.zeros)((B, T, D), dtype=torch.bfloat16, device=dev)
-                ldqo = D
+                q_out, ldqo, fresh = torch.empty((B, T, D), dtype=torch.bfloat16, device=dev), D, 1
             else:
                 ldqo = _rows("q_out", q_out, B, T, D, dev)
         if B == 0 or T == 0:
             return q_out
         _check(lib().wan_op_kv_append(k.data_ptr(), ldk, v.data_ptr(), ldv, B, T, heads, start.data_ptr(), _ptr(count),
                                       _ptr(k_gain), eps, 1 if rope else 0, frame[0], frame[1], split[0], split[1], split[2],
-                                      theta, _ptr(q), ldq, _ptr(q_gain), _ptr(q_out), ldqo, C.byref(c), st),
+                                      theta, _ptr(q), ldq, _ptr(q_gain), _ptr(q_out), ldqo, fresh, C.byref(c), st),
                "wan_op_kv_append")
     return q_out
 

@@ -49,7 +49,8 @@ constexpr float SCORE_TINY = 1e-36f;            // below it scores lose bits to 
 struct MeanOut {
     double* mean;           // [B, heads, blocks, 128]
     __half* unit;           // [B, heads, blocks, 128], null: not wanted
-    float* norm;            // [B, heads, blocks]
+    float* norm;            // [B, heads, norm_pitch]
+    int norm_pitch;
 };
 template <int RG>
 __global__ void __launch_bounds__(256) block_mean_kernel(const __nv_bfloat16* __restrict__ q, long long ldq,
@@ -67,7 +68,8 @@ __global__ void __launch_bounds__(256) block_mean_kernel(const __nv_bfloat16* __
     const int f0 = blk / (nH * nW) * box[0], i0 = blk / nW % nH * box[1], j0 = blk % nW * box[2];
     const int ef = min(box[0], F - f0), ei = min(box[1], H - i0), ej = min(box[2], W - j0);
     const int n = ef * ei * ej;
-    for (int t = threadIdx.y * blockDim.x + threadIdx.x; t < n; t += RG * blockDim.x)
+    const int y = RG > 1 ? threadIdx.y : 0;
+    for (int t = y * blockDim.x + threadIdx.x; t < n; t += RG * blockDim.x)
         tokens[t] = ((f0 + t / (ej * ei)) * H + i0 + t / ej % ei) * W + j0 + t % ej;
     __syncthreads();
     const int col = (blockIdx.y * blockDim.x + threadIdx.x) * 8;
@@ -92,7 +94,7 @@ __global__ void __launch_bounds__(256) block_mean_kernel(const __nv_bfloat16* __
 #pragma unroll
         for (int c = 0; c < 8; ++c) acc[c] += (double)s[c];
     };
-    int t = threadIdx.y * 8;
+    int t = y * 8;
     for (; t + 8 <= n; t += 8 * RG) {
         uint4 v[2][4];
 #pragma unroll
@@ -100,7 +102,7 @@ __global__ void __launch_bounds__(256) block_mean_kernel(const __nv_bfloat16* __
         add(v[0]);
         add(v[1]);
     }
-    for (const int last = min(n, t + 8); t < last; t += 4) {  // one group at most comes to a rest
+    for (const int last = RG > 1 ? min(n, t + 8) : n; t < last; t += 4) {  // one group at most comes to a rest
         uint4 v[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u)
@@ -109,12 +111,12 @@ __global__ void __launch_bounds__(256) block_mean_kernel(const __nv_bfloat16* __
     }
     if constexpr (RG > 1) {
         __shared__ double part[RG - 1][8][64];
-        if (threadIdx.y > 0) {
+        if (y > 0) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c) part[threadIdx.y - 1][c][threadIdx.x] = acc[c];
+            for (int c = 0; c < 8; ++c) part[y - 1][c][threadIdx.x] = acc[c];
         }
         __syncthreads();
-        if (threadIdx.y > 0) return;
+        if (y > 0) return;
 #pragma unroll
         for (int r = 0; r < RG - 1; ++r)
 #pragma unroll
@@ -147,7 +149,7 @@ __global__ void __launch_bounds__(256) block_mean_kernel(const __nv_bfloat16* __
         u[c] = *reinterpret_cast<const uint32_t*>(&h);
     }
     *reinterpret_cast<uint4*>(o.unit + at * 128 + col % 128) = make_uint4(u[0], u[1], u[2], u[3]);
-    if ((threadIdx.x & 15) == 0) o.norm[at] = (float)norm;
+    if ((threadIdx.x & 15) == 0) o.norm[((long long)b * heads + col / 128) * o.norm_pitch + blk] = (float)norm;
 }
 
 // ---------------------------------------------------------------- two-stage path
@@ -213,7 +215,7 @@ __global__ void __launch_bounds__(128) block_score_kernel(const __half* __restri
     for (int j = 0; j < 4; ++j) {
         const int col = k0 + n0 + 8 * j + (lane & 3) * 2;  // even, as the pitch is
         if (col >= nk) continue;
-        const float s0 = __ldg(kn + bh * nk + col), s1 = col + 1 < nk ? __ldg(kn + bh * nk + col + 1) : 0.f;
+        const float s0 = __ldg(kn + bh * pitch + col), s1 = col + 1 < nk ? __ldg(kn + bh * pitch + col + 1) : 0.f;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -313,7 +315,7 @@ __global__ void __launch_bounds__(128) block_score64_kernel(const double* __rest
 struct TopkParams {
     const float* scores;            // [B heads nq, pitch]
     const double *qm, *km;          // means
-    const float *qn, *kn;           // their norms
+    const float *qn, *kn;           // their norms: [B heads, nq], [B heads, pitch]
     const uint8_t* mask;            // [nq, nk] or null
     unsigned long long* exact;      // [rows, nk]: used by rows with many close scores only
     int nq, nk, pitch, topk;
@@ -322,50 +324,79 @@ struct TopkParams {
 template <int NPL>
 __global__ void __launch_bounds__(128) block_topk_kernel(const __grid_constant__ TopkParams p) {
     using Bits = typename std::conditional<(NPL > 32), unsigned long long, uint32_t>::type;
+    // rows come in coalesced and are read back a lane's consecutive blocks at a time
     __shared__ int again[4][32];
+    __shared__ float4 norms[NPL * 8], stage[4][NPL * 8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int nk = p.nk, j0 = lane * NPL;  // the lane's first block
     const long long bh = blockIdx.y;
     const int i_q = blockIdx.x * 4 + warp;
-    if (i_q >= p.nq) return;
     const long long row = bh * p.nq + i_q;
-    uint32_t key[NPL];
+    bool number = true;  // every norm of the head is one
+    for (int i = threadIdx.x; i < NPL * 8; i += 128) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < p.pitch / 4) {
+            v = __ldg(reinterpret_cast<const float4*>(p.kn + bh * p.pitch) + i);
+            const int rest = nk - 4 * i;
+            number = number && v.x < INFINITY && (rest < 2 || v.y < INFINITY) && (rest < 3 || v.z < INFINITY) &&
+                     (rest < 4 || v.w < INFINITY);
+        }
+        norms[i] = v;
+    }
+    if (i_q < p.nq) {
+        const float4* src = reinterpret_cast<const float4*>(p.scores + row * p.pitch);
+#pragma unroll
+        for (int i = 0; i < NPL / 4; ++i)
+            if (i * 32 + lane < p.pitch / 4) stage[warp][i * 32 + lane] = __ldg(src + i * 32 + lane);
+    }
+    number = __syncthreads_and(number);
+    if (i_q >= p.nq) return;
+    // scores of the allowed blocks; NaN, which no comparison holds for, where there is none or
+    // it is not the score that decides: `extra` are the blocks asked for
+    float f[NPL];
+    Bits extra = 0;
 #pragma unroll
     for (int i = 0; i < NPL; i += 4) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (j0 + i < nk) v = __ldg(reinterpret_cast<const float4*>(p.scores + row * p.pitch + j0 + i));
-        key[i] = j0 + i < nk ? score_key32(v.x) : 0u;
-        key[i + 1] = j0 + i + 1 < nk ? score_key32(v.y) : 0u;
-        key[i + 2] = j0 + i + 2 < nk ? score_key32(v.z) : 0u;
-        key[i + 3] = j0 + i + 3 < nk ? score_key32(v.w) : 0u;
+        const float4 v = stage[warp][(j0 + i) / 4];
+        const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) f[i + c] = j0 + i + c < nk ? (x[c] == x[c] ? x[c] : -INFINITY) : NAN;
     }
     if (p.mask) {
         const uint8_t* mrow = p.mask + (long long)i_q * nk + j0;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
             const uint8_t m = j0 + i < nk ? __ldg(mrow + i) : 0;
-            key[i] = m == 0 ? 0u : m == 1 ? key[i] : ~0u;
+            f[i] = m == 1 ? f[i] : NAN;
+            extra |= (Bits)(m > 1) << i;
         }
     }
-    auto count = [&](uint32_t at) {  // keys >= at
+    auto bits_of = [](Bits x) { return NPL > 32 ? __popcll(x) : __popc((uint32_t)x); };
+    auto count = [&](float at) {  // scores >= at
         int n = 0;
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) n += key[i] >= at;
+        for (int i = 0; i < NPL; ++i) n += f[i] >= at;
         return (int)__reduce_add_sync(0xffffffffu, n);
     };
-    const int allowed = count(1), always = p.mask ? count(~0u) : 0;
-    const int take = min(p.topk, allowed);
+    const int always = p.mask ? __reduce_add_sync(0xffffffffu, bits_of(extra)) : 0;
+    const int scored = p.mask ? count(-INFINITY) : nk;
+    const int take = min(p.topk, always + scored);
+    const int want = take - always;  // of the scored ones
     int* dst = p.blocks + row * p.topk;
-    // the lane's picks to their places: ascending, after those of the lanes before
-    auto put = [&](Bits picks) {
-        const int mine = NPL > 32 ? __popcll(picks) : __popc((uint32_t)picks);
-        int to = mine;
+    // set bits of the lanes before
+    auto before = [&](Bits bits) {
+        const int mine = bits_of(bits);
+        int n = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, to, o);
-            if (lane >= o) to += v;
+            const int v = __shfl_up_sync(0xffffffffu, n, o);
+            if (lane >= o) n += v;
         }
-        to -= mine;
+        return n - mine;
+    };
+    // the picks to their places, ascending
+    auto put = [&](Bits picks) {
+        int to = before(picks);
         while (picks) {
             const int i = NPL > 32 ? __ffsll((long long)picks) - 1 : __ffs((int)picks) - 1;
             picks &= picks - 1;
@@ -376,96 +407,96 @@ __global__ void __launch_bounds__(128) block_topk_kernel(const __grid_constant__
     };
     // picks among equals: the first `left` of the set bits, lanes in order
     auto first_of = [&](Bits bits, int left) -> Bits {
-        const int mine = NPL > 32 ? __popcll(bits) : __popc((uint32_t)bits);
-        int before = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, before, o);
-            if (lane >= o) before += v;
-        }
-        before -= mine;
         Bits out = 0;
-        for (int n = before; bits && n < left; ++n) {
+        for (int n = before(bits); bits && n < left; ++n) {
             const Bits low = bits & (~bits + 1);
             out |= low;
             bits ^= low;
         }
         return out;
     };
-    if (take == allowed || always >= take) {  // all that is allowed, or only blocks asked for
-        Bits bits = 0;
-        const uint32_t from = take == allowed ? 1u : ~0u;
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) bits |= (Bits)(key[i] >= from) << i;
-        put(first_of(bits, take));
+    if (want <= 0) {  // blocks asked for alone, the lowest of them
+        put(first_of(extra, take));
         return;
     }
-    // lo: a key that at least `take` keys reach; hi: one that fewer exceed
-    uint32_t lo = ~0u, hi = 0;
+    if (want == scored) {  // all that is allowed
+        Bits all = extra;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) all |= (Bits)(f[i] == f[i]) << i;
+        put(all);
+        return;
+    }
+    // at: a score that `want` scores reach, and no more unless equal ones lie at the border.  The
+    // next place is taken by the counts and half way in turn; where that does not settle it
+    // (infinities, scores of many magnitudes) half way between the scores' bit patterns.
+    float lo = INFINITY, hi = -INFINITY;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
-        lo = min(lo, key[i] - 1);  // 0 wraps to the largest
-        hi = max(hi, key[i] == ~0u ? 0u : key[i]);
+        lo = fminf(lo, f[i]);
+        hi = fmaxf(hi, f[i]);
     }
-    lo = __reduce_min_sync(0xffffffffu, lo) + 1;
-    hi = __reduce_max_sync(0xffffffffu, hi);
-    uint32_t at = lo;
-    int n_at = allowed, n_hi = always;
-    for (int step = 0; n_at != take && lo < hi; ++step) {
-        uint32_t mid = lo + ((hi - lo) >> 1) + 1;
-        if (step < 24) {  // between the scores; a place by the counts every other step
-            const float a = key32_score(lo), b = key32_score(hi);
-            const float part = step & 1 ? 0.5f : fminf(fmaxf((float)(n_at - take) / (float)(n_at - n_hi), 0.1f), 0.9f);
-            const uint32_t m = score_key32(a + part * (b - a));
-            if (m > lo && m <= hi) mid = m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
+    float at = lo;
+    int n_at = scored, n_hi = 0;  // n_hi: scores >= the last place that was too high
+    for (int step = 0; n_at != want && lo < hi; ++step) {
+        const float part = step & 1 ? 0.5f : fminf(fmaxf((float)(n_at - want) / (float)(n_at - n_hi), 0.1f), 0.9f);
+        float mid = lo + part * (hi - lo);
+        if (step >= 24 || !(mid > lo && mid <= hi)) {
+            const uint32_t a = score_key32(lo), b = score_key32(hi);
+            mid = key32_score(a + ((b - a) >> 1) + 1);
         }
         const int n = count(mid);
-        if (n >= take) {
-            lo = mid;
-            at = mid;
+        if (n >= want) {
+            lo = at = mid;
             n_at = n;
         } else {
-            hi = mid - 1;
+            hi = key32_score(score_key32(mid) - 1);  // the next lower float
             n_hi = n;
         }
     }
     // L, U and the close ones
-    const float* kn = p.kn + bh * nk + j0;
-    float L = INFINITY, U = -INFINITY;
-    uint32_t vk = ~0u;
+    const float4* kn = norms + j0 / 4;
+    float L = INFINITY, U = -INFINITY, vk = INFINITY;
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) vk = min(vk, key[i] >= at ? key[i] : ~0u);
-    vk = __reduce_min_sync(0xffffffffu, vk);
-    bool number = p.qn[row] < INFINITY;
+    for (int i = 0; i < NPL; ++i) vk = fminf(vk, f[i] >= at ? f[i] : INFINITY);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) vk = fminf(vk, __shfl_xor_sync(0xffffffffu, vk, o));
+    float d[4];
+    auto bounds = [&](int i) {  // of four blocks
+        const float4 v = kn[i / 4];
+        d[0] = fmaf(SCORE_ERROR, v.x, SCORE_TINY);
+        d[1] = fmaf(SCORE_ERROR, v.y, SCORE_TINY);
+        d[2] = fmaf(SCORE_ERROR, v.z, SCORE_TINY);
+        d[3] = fmaf(SCORE_ERROR, v.w, SCORE_TINY);
+    };
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
-        if (key[i] == 0 || key[i] == ~0u) continue;
-        const float d = fmaf(SCORE_ERROR, __ldg(kn + i), SCORE_TINY), a = key32_score(key[i]);
-        number = number && d < INFINITY;
-        if (key[i] >= at) L = fminf(L, a - d);
-        if (key[i] <= vk) U = fmaxf(U, a + d);
+        if (i % 4 == 0) bounds(i);
+        L = fminf(L, f[i] >= at ? f[i] - d[i % 4] : INFINITY);
+        U = fmaxf(U, f[i] <= vk ? f[i] + d[i % 4] : -INFINITY);
     }
-    number = __all_sync(0xffffffffu, number);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         L = fminf(L, __shfl_xor_sync(0xffffffffu, L, o));
         U = fmaxf(U, __shfl_xor_sync(0xffffffffu, U, o));
     }
-    if (!number) {  // a mean is not finite: all are close
-        L = -INFINITY;
-        U = INFINITY;
-    }
-    Bits sure = 0, close = 0;
+    Bits sure = extra, close = 0;
+    if (number && p.qn[row] < INFINITY) {
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-        if (key[i] == 0) continue;
-        const float d = key[i] == ~0u ? 0.f : fmaf(SCORE_ERROR, __ldg(kn + i), SCORE_TINY);
-        const float a = key32_score(key[i]);
-        const bool in = key[i] == ~0u || a - d > U;
-        sure |= (Bits)in << i;
-        close |= (Bits)(!in && !(a + d < L)) << i;
+        for (int i = 0; i < NPL; ++i) {
+            if (i % 4 == 0) bounds(i);
+            const bool in = f[i] - d[i % 4] > U;
+            sure |= (Bits)in << i;
+            close |= (Bits)(!in && f[i] + d[i % 4] >= L) << i;
+        }
+    } else {  // a mean is not finite: all are close
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) close |= (Bits)(f[i] == f[i]) << i;
     }
-    auto bits_of = [](Bits x) { return NPL > 32 ? __popcll(x) : __popc((uint32_t)x); };
     const int n_sure = __reduce_add_sync(0xffffffffu, bits_of(sure));
     const int n_close = __reduce_add_sync(0xffffffffu, bits_of(close));
     const int need = take - n_sure;
@@ -493,14 +524,7 @@ __global__ void __launch_bounds__(128) block_topk_kernel(const __grid_constant__
     };
     if (n_close <= 32) {
         // lane n ranks the n-th close block among all of them
-        const int mine = bits_of(close);
-        int first = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, first, o);
-            if (lane >= o) first += v;
-        }
-        first -= mine;
+        const int first = before(close);
         Bits rest = close;
         for (int n = first; rest; ++n) {
             const Bits low = rest & (~rest + 1);
@@ -689,7 +713,8 @@ int block_select_max_blocks() { return TOPK64_SMEM / 8; }
 long long block_select_workspace(int B, int heads, const BlockGrid& g) {
     const long long nq = g.q_blocks(), nk = g.k_blocks();
     const long long means = (nq + nk) * 128 * 8 + nq * nk * 8;
-    const long long fast = nk <= MAX_FAST ? (nq + nk) * (128 * 2 + 4) + nq * ((nk + 3) / 4 * 4) * 4 : 0;
+    const long long pitch = (nk + 3) / 4 * 4;
+    const long long fast = nk <= MAX_FAST ? (nq + nk) * 128 * 2 + (nq + pitch + nq * pitch) * 4 : 0;
     return (long long)B * heads * (means + fast) + 64;
 }
 
@@ -710,7 +735,7 @@ cudaError_t launch_block_select(const void* q, long long ldq, const void* k, lon
     double* qm = reinterpret_cast<double*>(ws);
     double* km = qm + bh * nq * 128;
     unsigned long long* keys = reinterpret_cast<unsigned long long*>(km + bh * nk * 128);  // [rows, nk]
-    MeanOut oq{qm, nullptr, nullptr}, ok{km, nullptr, nullptr};
+    MeanOut oq{qm, nullptr, nullptr, 0}, ok{km, nullptr, nullptr, 0};
     float* scores = nullptr;
     const int pitch = (nk + 3) / 4 * 4;
     if (fast) {
@@ -718,8 +743,10 @@ cudaError_t launch_block_select(const void* q, long long ldq, const void* k, lon
         oq.unit = reinterpret_cast<__half*>(at);
         ok.unit = oq.unit + bh * nq * 128;
         scores = reinterpret_cast<float*>(ok.unit + bh * nk * 128);
-        oq.norm = scores + rows * pitch;
-        ok.norm = oq.norm + bh * nq;
+        ok.norm = scores + rows * pitch;
+        ok.norm_pitch = pitch;
+        oq.norm = ok.norm + bh * pitch;
+        oq.norm_pitch = nq;
     }
     const int vecs = heads * 16;
     auto mean = [&](auto kernel, int most, int groups) {

@@ -163,11 +163,13 @@ int block_select_max_blocks();  // key blocks per row at most
 cudaError_t init_block_select_attributes();
 
 // Keys (optionally RMS-normed and rotated) and values of T new tokens per
-// sequence into cache places start[b] + t; q (may be null) likewise into q_out.
+// sequence into cache places start[b] + t; q (may be null) likewise into q_out, whose
+// other rows are zeroed (zero_rest) or left.
 cudaError_t launch_kv_append(const void* k, long long ldk, const void* v, long long ldv, int B, int T, int heads,
                              const int* start, const int* count, const float* k_gain, float eps, int rope, int H, int W,
                              int rope_t, int rope_h, int rope_w, double theta, const void* q, long long ldq,
-                             const float* q_gain, void* q_out, long long ldqo, const KvPages& c, const LaunchCtx& ctx);
+                             const float* q_gain, void* q_out, long long ldqo, int zero_rest, const KvPages& c,
+                             const LaunchCtx& ctx);
 
 // buf[r, 0:D) *= the RMSNorm row factor of rn (in place, bf16, one rounding).
 cudaError_t launch_rms_apply(void* buf, long long ld, int rows, int D, const RowNorm& rn, const LaunchCtx& ctx);

@@ -29,7 +29,7 @@ struct AppendParams {
     const int *start, *count;
     const float *k_gain, *q_gain;
     float eps;
-    int rope, H, W;
+    int rope, H, W, zero_rest;
     int nt, nh;             // pairs of the frame and row axes
     KvPages c;
     int log_page;
@@ -58,14 +58,21 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const __grid_constant
     if (row >= (long long)p.B * p.T) return;
     const int b = (int)(row / p.T), t = (int)(row - (long long)b * p.T);
     const int first = __ldg(p.start + b);
-    if (p.count && t >= __ldg(p.count + b)) return;
+    auto vec = [&](int i) { return (i * WPR + sub) * 32 + lane; };
+    if (first < 0 || (p.count && t >= __ldg(p.count + b))) {
+        if (what == 2 && p.zero_rest) {
+            uint4* rest = reinterpret_cast<uint4*>(p.q_out + row * p.ldqo);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (vec(i) < vecs) rest[vec(i)] = make_uint4(0, 0, 0, 0);
+        }
+        return;
+    }
     const uint4* src = reinterpret_cast<const uint4*>(what == 0 ? p.k + row * p.ldk : what == 1 ? p.v + row * p.ldv
                                                                                                 : p.q + row * p.ldq);
-    auto vec = [&](int i) { return (i * WPR + sub) * 32 + lane; };
     uint4 x[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) x[i] = vec(i) < vecs ? src[vec(i)] : make_uint4(0, 0, 0, 0);
-    if (first < 0) return;
     const uint32_t slot = (uint32_t)first + (uint32_t)t;
     uint4* dst;
     if (what == 2) {
@@ -164,7 +171,8 @@ void append(const AppendParams& p, cudaStream_t stream) {
 cudaError_t launch_kv_append(const void* k, long long ldk, const void* v, long long ldv, int B, int T, int heads,
                              const int* start, const int* count, const float* k_gain, float eps, int rope, int H, int W,
                              int rope_t, int rope_h, int rope_w, double theta, const void* q, long long ldq,
-                             const float* q_gain, void* q_out, long long ldqo, const KvPages& c, const LaunchCtx& ctx) {
+                             const float* q_gain, void* q_out, long long ldqo, int zero_rest, const KvPages& c,
+                             const LaunchCtx& ctx) {
     AppendParams p{};
     p.k = reinterpret_cast<const __nv_bfloat16*>(k);
     p.v = reinterpret_cast<const __nv_bfloat16*>(v);
@@ -183,6 +191,7 @@ cudaError_t launch_kv_append(const void* k, long long ldk, const void* v, long l
     p.q_gain = q_gain;
     p.eps = eps;
     p.rope = rope;
+    p.zero_rest = zero_rest;
     p.H = H;
     p.W = W;
     p.nt = rope_t / 2;

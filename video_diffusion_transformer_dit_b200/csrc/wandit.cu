@@ -1497,7 +1497,8 @@ wan_status wan_op_attention_blocks(const void* q, int64_t ldq, const void* k, in
 wan_status wan_op_kv_append(const void* k, int64_t ldk, const void* v, int64_t ldv, int B, int T, int heads,
                             const int32_t* start, const int32_t* count, const float* k_gain, float eps, int rope, int H,
                             int W, int rope_t, int rope_h, int rope_w, float theta, const void* q, int64_t ldq,
-                            const float* q_gain, void* q_out, int64_t ldqo, const wan_kv_cache* cache, void* stream) {
+                            const float* q_gain, void* q_out, int64_t ldqo, int zero_rest, const wan_kv_cache* cache,
+                            void* stream) {
     if (!k || !v || !start || !cache || !cache->k || !cache->v || !cache->table || (q && !q_out)) return WAN_EINVAL;
     wan::KvPages pages;
     if (B < 0 || T < 0 || heads <= 0 || heads > 96 || (int64_t)B * T > (1ll << 31) || !kv_cache_ok(cache, heads, &pages))
@@ -1511,7 +1512,7 @@ wan_status wan_op_kv_append(const void* k, int64_t ldk, const void* v, int64_t l
     LaunchCtx ctx;
     if (!op_ctx(reinterpret_cast<cudaStream_t>(stream), &ctx)) return WAN_ECUDA;
     return op_status(wan::launch_kv_append(k, ldk, v, ldv, B, T, heads, start, count, k_gain, eps, rope, H, W, rope_t, rope_h,
-                                           rope_w, theta, q, ldq, q_gain, q_out, ldqo, pages, ctx));
+                                           rope_w, theta, q, ldq, q_gain, q_out, ldqo, zero_rest, pages, ctx));
 }
 
 int64_t wan_op_attention_paged_workspace(int B, int heads, int T, const wan_kv_cache* cache) {
