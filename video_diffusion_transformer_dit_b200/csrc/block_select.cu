@@ -322,7 +322,7 @@ struct TopkParams {
     int *blocks, *counts;
 };
 template <int NPL>
-__global__ void __launch_bounds__(128) block_topk_kernel(const __grid_constant__ TopkParams p) {
+__global__ void __launch_bounds__(128, NPL <= 24 ? 8 : 1) block_topk_kernel(const __grid_constant__ TopkParams p) {
     using Bits = typename std::conditional<(NPL > 32), unsigned long long, uint32_t>::type;
     // rows come in coalesced and are read back a lane's consecutive blocks at a time
     __shared__ int again[4][32];
@@ -427,24 +427,33 @@ __global__ void __launch_bounds__(128) block_topk_kernel(const __grid_constant__
         return;
     }
     // at: a score that `want` scores reach, and no more unless equal ones lie at the border.  The
-    // next place is taken by the counts and half way in turn; where that does not settle it
-    // (infinities, scores of many magnitudes) half way between the scores' bit patterns.
-    float lo = INFINITY, hi = -INFINITY;
+    // first place is where normally distributed scores would have it, the next ones are taken by
+    // the counts, every third half way (five counts for a normal row, ten without the first
+    // guess); where that does not settle it (infinities, scores of many magnitudes) half way
+    // between the scores' bit patterns.
+    float lo = INFINITY, hi = -INFINITY, sum = 0.f, sum2 = 0.f;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
         lo = fminf(lo, f[i]);
         hi = fmaxf(hi, f[i]);
+        const float x = f[i] == f[i] ? f[i] : 0.f;
+        sum += x;
+        sum2 = fmaf(x, x, sum2);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
         hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        sum2 += __shfl_xor_sync(0xffffffffu, sum2, o);
     }
+    const float mean = sum / scored, spread = sqrtf(fmaxf(sum2 / scored - mean * mean, 0.f));
+    const float guess = mean + spread * 0.4073f * log2f((float)(scored - want) / (float)want);  // ln 2 / 1.702
     float at = lo;
     int n_at = scored, n_hi = 0;  // n_hi: scores >= the last place that was too high
     for (int step = 0; n_at != want && lo < hi; ++step) {
-        const float part = step & 1 ? 0.5f : fminf(fmaxf((float)(n_at - want) / (float)(n_at - n_hi), 0.1f), 0.9f);
-        float mid = lo + part * (hi - lo);
+        const float part = step % 3 == 0 ? 0.5f : fminf(fmaxf((float)(n_at - want) / (float)(n_at - n_hi), 0.05f), 0.95f);
+        float mid = step == 0 && guess > lo && guess < hi ? guess : lo + part * (hi - lo);
         if (step >= 24 || !(mid > lo && mid <= hi)) {
             const uint32_t a = score_key32(lo), b = score_key32(hi);
             mid = key32_score(a + ((b - a) >> 1) + 1);
