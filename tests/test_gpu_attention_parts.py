@@ -598,3 +598,22 @@ def test_kv_append_zeroes_the_rest_of_a_new_query_buffer():
     assert bool((q_out[0, 4:] == 0).all()) and bool((q_out[1:] == 0).all())
     y, size = R.rotated(q[0, :4].to(DT), torch.arange(4, device="cuda"), heads, (3, 4), None)
     assert bool(((q_out[0, :4].to(DT) - y).abs() <= R.HALF_STEP * 1.001 * y.abs() + 2.0 ** -20 * size).all())
+
+
+def test_join_without_parts_ends_after_the_attention():
+    """Every sequence lies whole in one range, so the join kernel has nothing to do: what follows in the stream must
+    still find the attention's rows."""
+    heads, per, page, T = 2, 40, 64, 1
+    kc, vc, table = cache(8, per, page, heads, 142)
+    q = rnd((8, T, heads * 128), 143)
+    ln = torch.full((8,), 64, dtype=torch.int32, device="cuda")
+    assert B().op_attention_paged_workspace(8, heads, T, kc, vc, table) > 0
+    out, copies = torch.empty_like(q), []
+    for _ in range(20):
+        out.fill_(7.0)
+        B().op_attention_paged(q, kc, vc, table, ln, heads, out=out)
+        copies.append(out + 0)
+    B().op_sync()
+    ref, ref_lse, moved, size = R.attention_paged(q, kc, vc, table, ln, heads)
+    check(copies[0], None, ref, ref_lse, moved, size)
+    assert all(torch.equal(c, copies[0]) for c in copies)

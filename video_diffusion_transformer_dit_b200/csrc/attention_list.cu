@@ -755,6 +755,7 @@ __global__ void __launch_bounds__(256) list_join_kernel(const __grid_constant__ 
     const int Lq = MODE == alist::BLOCKS ? p.g.q_tokens() : p.T;
     int s0 = 0, s1 = p.splits - 1;
     bool inside = false;  // pages: the first part begins inside its range
+    bool parts = true;    // else written whole by its unit
     if (MODE == alist::PAGES) {
         uint32_t first = 0, total = 0, mine = 0;
         for (int i = lane; i < p.B; i += 32) {
@@ -766,23 +767,27 @@ __global__ void __launch_bounds__(256) list_join_kernel(const __grid_constant__ 
         first = __reduce_add_sync(0xffffffffu, first);
         total = __reduce_add_sync(0xffffffffu, total);
         mine = __reduce_add_sync(0xffffffffu, mine);
-        if (mine == 0) return;
         // range that holds tile x: the largest r with floor(r total / ranges) <= x
         const uint32_t ranges = page_ranges(p, total);
         auto range_of = [&](uint32_t x) {
             return (int)(((x + 1ull) * ranges + total - 1) / total) - 1;
         };
-        s0 = range_of(first);
-        s1 = range_of(first + mine - 1);
-        if (s0 == s1) return;  // whole in one range: written by its unit
-        inside = (uint32_t)((unsigned long long)total * s0 / ranges) < first;
+        if (mine > 0) {
+            s0 = range_of(first);
+            s1 = range_of(first + mine - 1);
+            inside = (uint32_t)((unsigned long long)total * s0 / ranges) < first;
+        }
+        parts = mine > 0 && s0 != s1;
     }
     auto part = [&](int s) -> long long {
         if (MODE == alist::BLOCKS) return (long long)s * per + unit;
         const long long u = (long long)s * (p.nqb * p.heads) + h * p.nqb + qt;
         return u * 2 + (s == s0 && inside);
     };
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written
+    // The parts are written.  Every CTA waits, also one with nothing to join: work
+    // behind this kernel in the stream counts on the attention kernel's end.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!parts) return;
     int token[2];
     float l[2];
 #pragma unroll
