@@ -600,6 +600,36 @@ def test_kv_append_zeroes_the_rest_of_a_new_query_buffer():
     assert bool(((q_out[0, :4].to(DT) - y).abs() <= R.HALF_STEP * 1.001 * y.abs() + 2.0 ** -20 * size).all())
 
 
+def test_block_select_keeps_what_large_tokens_hide():
+    """Tokens of 2^30 that cancel inside a block beside ones of about 1: the scores are what the small ones leave
+    (fp32 sums would lose all of them)."""
+    for nk, vol in ((90, 64), (17, 16)):
+        q = torch.ones((1, 64, 128), dtype=torch.bfloat16, device="cuda")
+        k = torch.zeros((1, nk, vol, 128), dtype=torch.bfloat16, device="cuda")
+        k[:, :, 0::4] = 2.0 ** 30
+        k[:, :, 2::4] = -2.0 ** 30
+        value = torch.randperm(nk, generator=torch.Generator().manual_seed(141)).to("cuda", torch.bfloat16)
+        k[:, :, 1::4] = value.view(1, nk, 1, 1)
+        args = (1, (1, 1, 64), (1, 1, nk * vol), (1, 1, 64), (1, 1, vol))
+        blocks, counts = B().op_block_select(q, k.view(1, nk * vol, 128), *args, 5)
+        B().op_sync()
+        best = value.float().argsort(descending=True)[:5].sort().values.int()
+        assert counts.item() == 5 and torch.equal(blocks.view(-1), best)
+
+
+@pytest.mark.parametrize("nk", [30, 200])
+def test_block_select_sums_past_the_range_of_fp32(nk):
+    """Tokens near bf16's largest value of one sign: their sum leaves fp32's range, their mean does not."""
+    q = torch.full((1, 64, 128), 2.0 ** -100, dtype=torch.bfloat16, device="cuda")
+    value = (1 + torch.randperm(nk, generator=torch.Generator().manual_seed(144)) % 100 / 128).to("cuda", torch.bfloat16)
+    k = torch.zeros((1, nk, 16, 128), dtype=torch.bfloat16, device="cuda")
+    k[..., 0] = value.view(1, nk, 1) * 2.0 ** 127
+    args = (1, (1, 1, 64), (1, 1, nk * 16), (1, 1, 64), (1, 1, 16))
+    blocks, counts = B().op_block_select(q, k.view(1, nk * 16, 128), *args, 7)
+    B().op_sync()
+    best = value.float().argsort(descending=True, stable=True)[:7].sort().values.int()
+    assert counts.item() == 7 and torch.equal(blocks.view(-1), best)
+
 def test_join_without_parts_ends_after_the_attention():
     """Every sequence lies whole in one range, so the join kernel has nothing to do: what follows in the stream must
     still find the attention's rows."""

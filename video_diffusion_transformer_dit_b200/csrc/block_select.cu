@@ -41,11 +41,14 @@ constexpr float SCORE_TINY = 1e-36f;            // below it scores lose bits to 
 
 // Means of the blocks of q (first g.q_blocks() CTAs) and k, per head: fp64, fp16 of
 // unit length, and norm (NaN or infinite where a mean is).  One CTA per block and
-// column slice, eight columns per thread; where there are few of them (a small
-// grid) RG = 4 groups of threads take every fourth eight tokens each: a block is a
-// chain of loads, 14 -> 9 us at 15 blocks; four tokens are added in fp32 before they join the
-// fp64 sum: bf16 has 8 significant bits, so a sum of four of them is exact in
-// fp32's 24 unless their exponents lie 14 apart.
+// column slice, eight columns per thread, four tokens loaded while the four before
+// are added; where there are few CTAs (a small grid) RG = 4 groups of threads take
+// every fourth eight tokens each: a block is a chain of loads (14.5 -> 7.6 us at 15
+// blocks).  Every token is added in fp64: it must not matter what stands beside a
+// small one.  (Sums of four tokens in fp32 first, which lose a value 2^17 times
+// smaller than its neighbour, took 70 us where this takes 72; the same with the
+// rounding errors kept beside them 133.)  The conversions to fp64, at 16 a clock and
+// SM, are two thirds busy then; the loads are what bounds it.
 struct MeanOut {
     double* mean;           // [B, heads, blocks, 128]
     __half* unit;           // [B, heads, blocks, 128], null: not wanted
@@ -80,34 +83,39 @@ __global__ void __launch_bounds__(256) block_mean_kernel(const __nv_bfloat16* __
 #pragma unroll
     for (int c = 0; c < 8; ++c) acc[c] = 0.0;
     auto add = [&](const uint4 (&v)[4]) {
-        float s[8];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const float2 p = unpack_bf16(w[c]);
-                s[2 * c] = u ? s[2 * c] + p.x : p.x;
-                s[2 * c + 1] = u ? s[2 * c + 1] + p.y : p.y;
+                acc[2 * c] += (double)p.x;
+                acc[2 * c + 1] += (double)p.y;
             }
         }
-#pragma unroll
-        for (int c = 0; c < 8; ++c) acc[c] += (double)s[c];
     };
-    int t = y * 8;
-    for (; t + 8 <= n; t += 8 * RG) {
-        uint4 v[2][4];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) v[u >> 2][u & 3] = __ldg(reinterpret_cast<const uint4*>(base + (long long)tokens[t + u] * ld));
-        add(v[0]);
-        add(v[1]);
-    }
-    for (const int last = RG > 1 ? min(n, t + 8) : n; t < last; t += 4) {  // one group at most comes to a rest
-        uint4 v[4];
+    auto fetch = [&](int t, uint4 (&v)[4]) {
 #pragma unroll
         for (int u = 0; u < 4; ++u)
             v[u] = t + u < n ? __ldg(reinterpret_cast<const uint4*>(base + (long long)tokens[t + u] * ld)) : make_uint4(0, 0, 0, 0);
-        add(v);
+    };
+    if (RG == 1) {
+        uint4 a[4], b[4];  // past the end fetch() gives zeros
+        fetch(0, a);
+        for (int t = 0; t < n; t += 8) {
+            fetch(t + 4, b);
+            add(a);
+            fetch(t + 8, a);
+            add(b);
+        }
+    } else {
+        for (int t = y * 8; t < n; t += 8 * RG) {
+            uint4 a[4], b[4];
+            fetch(t, a);
+            fetch(t + 4, b);
+            add(a);
+            add(b);
+        }
     }
     if constexpr (RG > 1) {
         __shared__ double part[RG - 1][8][64];
