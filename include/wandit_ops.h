@@ -4,8 +4,9 @@
  * These launch, one at a time, the same sm_100a kernels that wan_dit_forward()
  * strings together, so each step of the Wan DiT forward can be checked on its
  * own, and the attention operators over parts of the sequence (selected key
- * blocks, a paged cache), which the forward does not call.  Citations name the page and section whose computation the kernel
- * performs (see wandit.h for the page list).  Conventions are those of
+ * blocks, a paged cache), which the forward does not call.  Citations name the
+ * page and section whose computation the kernel performs (see wandit.h for the
+ * page list).  Conventions are those of
  * wandit.h: plain device pointers, `stream` is a cudaStream_t as void*, calls
  * are asynchronous, nothing is retained after the call, shape errors are
  * reported before any launch, and wan_op_sync() reports a kernel wait that ran
@@ -117,8 +118,12 @@ WANDIT_API wan_status wan_op_attention_qnorm(const void* q, int64_t ldq, const v
  * them; a plain sequence of L tokens is the grid 1 x 1 x L).  Boxes of qb_F x
  * qb_H x qb_W query tokens and kb_F x kb_H x kb_W key tokens cut the grids into
  * blocks, numbered like the tokens; the blocks at a grid's far edges hold the
- * tokens that are left.  Limits: every extent >= 1; at most 128 tokens per query
- * block; 16, 32, 64 or 128 per key block (the box's volume).                 */
+ * tokens that are left.  Limits: every extent >= 1; at most 2^30 tokens per grid
+ * and 2^31 in all samples; at most 128 tokens per query block; 16, 32, 64 or 128
+ * per key block (the box's volume).
+ * All calls of this section may be captured into a graph and replayed; the first
+ * op call on a device allocates its error flag, so one has to run before a
+ * capture.                                                                   */
 typedef struct {
     int q_F, q_H, q_W;      /* query token grid                                */
     int k_F, k_H, k_W;      /* key token grid                                  */
@@ -163,7 +168,8 @@ WANDIT_API int64_t wan_op_block_select_workspace(int B, int heads, const wan_blo
  *   workspace  as above, wan_op_attention_blocks_workspace() bytes; may be NULL
  *         where that is 0 (it is, unless the query tiles are too few to fill the
  *         GPU: then each list is split and the parts are joined)
- * Layouts as wan_op_attention; errors as wan_op_block_select (topk >= 1).     */
+ * Layouts as wan_op_attention; errors as wan_op_block_select (topk in [1, 2^24],
+ * blocks may list more than the grid has).                                    */
 WANDIT_API wan_status wan_op_attention_blocks(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v,
                                               int64_t ldv, void* o, int64_t ldo, int B, int heads,
                                               const wan_block_grid* g, const int32_t* blocks, const int32_t* counts,
@@ -176,7 +182,8 @@ WANDIT_API int64_t wan_op_attention_blocks_workspace(int B, int heads, const wan
  * in columns [128 h, 128 h + 128)), and at the same place of v.  Place s of
  * sequence b lies in page table[b * table_ld + s / page_size], at s % page_size.
  * Table entries outside [0, num_pages) hold nothing: they are not written, and
- * attention skips their places.  page_size 16, 32, 64 or 128.                */
+ * attention skips their places.  page_size 16, 32, 64 or 128; max_pages *
+ * page_size at most 2^29.                                                    */
 typedef struct {
     void* k;
     void* v;
@@ -200,10 +207,11 @@ typedef struct {
  * are zeroed if zero_rest != 0 (for a buffer that is not q itself) or left.  Two
  * sequences that share a page must not write the same place.
  * Errors before any launch: WAN_EINVAL for a null pointer, WAN_ESHAPE for B, T <
- * 0, heads outside [1, 96], a RoPE split that is not even with sum 128, H, W <= 0, theta <=
- * 0, strides or pointers (k, v, q, q_out, the cache, gains) that are not
- * 16-byte aligned, a leading dimension or token stride below 128 * heads, a
- * page stride that lets pages overlap, or a cache outside the limits above.   */
+ * 0, B * T > 2^31, heads outside [1, 96], a RoPE split that is not even with sum
+ * 128, H, W <= 0, H * W > 2^30, theta <= 0, strides or pointers (k, v, q, q_out,
+ * the cache, gains) that are not 16-byte aligned, a leading dimension or token
+ * stride below 128 * heads, a page stride that lets pages overlap, or a cache
+ * outside the limits above.                                                  */
 WANDIT_API wan_status wan_op_kv_append(const void* k, int64_t ldk, const void* v, int64_t ldv, int B, int T, int heads,
                                        const int32_t* start, const int32_t* count, const float* k_gain, float eps,
                                        int rope, int H, int W, int rope_t, int rope_h, int rope_w, float theta,
@@ -218,7 +226,10 @@ WANDIT_API wan_status wan_op_kv_append(const void* k, int64_t ldk, const void* v
  * (f32 [B, heads, T], or NULL).  Memory of a page past the sequence's end is not
  * read into the result, whatever it holds.  Long caches are split and joined when
  * the query tiles are few: workspace as above,
- * wan_op_attention_paged_workspace() bytes.                                  */
+ * wan_op_attention_paged_workspace() bytes.  Errors before any launch: WAN_EINVAL
+ * for a null pointer, WAN_ESHAPE for B, T < 0, B * T > 2^30, B * heads > 2^20,
+ * strides, pointers or a cache outside the limits above, or a workspace that is
+ * too small.                                                                 */
 WANDIT_API wan_status wan_op_attention_paged(const void* q, int64_t ldq, const wan_kv_cache* cache,
                                              const int32_t* lens, void* o, int64_t ldo, int B, int heads, int T,
                                              float* lse, void* workspace, int64_t workspace_bytes, void* stream);

@@ -155,3 +155,25 @@ def test_python_wrappers_refuse_tensors_that_do_not_fit():
         binding.op_attention_paged(x, c, c, t, t[0, :1], 2)
     with pytest.raises(ValueError):
         binding.op_kv_append(x, x, c, c, t, t[0, :1], 2, (8, 8))
+
+
+def test_lists_beyond_the_index_range_are_refused(lib):
+    g = grid()
+    for topk in ((1 << 24) + 1, 1 << 30, (1 << 31) - 1):
+        assert lib.wan_op_attention_blocks_workspace(1, 2, C.byref(g), topk) == -1
+        assert lib.wan_op_attention_blocks(FAKE, 256, FAKE, 256, FAKE, 256, FAKE, 256, 1, 2, C.byref(g), FAKE, FAKE, topk,
+                                           None, FAKE, BIG, None) == ESHAPE
+    assert lib.wan_op_attention_blocks_workspace(1, 2, C.byref(g), 1 << 24) >= 0
+
+
+def test_python_wrappers_refuse_grids_and_streams_that_do_not_fit(lib):
+    import types
+
+    import torch
+    from video_diffusion_transformer_dit_b200 import binding
+    for d in (((8, 8), (3, 8, 8), (1, 8, 8), (1, 4, 4)), ((3, 8, 8, 1), (3, 8, 8), (1, 8), (1, 4, 4)),
+              ((3, 8, 8), (3, 8, 8), (1, 8, 8), (16,))):
+        with pytest.raises(ValueError, match="frames, rows, columns"):
+            binding.op_block_select_workspace(1, 2, *d)
+    with pytest.raises(ValueError, match="stream of cuda:0"):
+        binding._on(torch.device("cuda", 0), types.SimpleNamespace(device=torch.device("cuda", 1)))

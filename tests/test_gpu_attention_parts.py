@@ -647,3 +647,45 @@ def test_join_without_parts_ends_after_the_attention():
     ref, ref_lse, moved, size = R.attention_paged(q, kc, vc, table, ln, heads)
     check(copies[0], None, ref, ref_lse, moved, size)
     assert all(torch.equal(c, copies[0]) for c in copies)
+
+
+def test_selection_and_split_attention_captured_and_replayed():
+    """Selection, then attention over few query tiles (its lists are split and joined), captured with q, k and v
+    that change between replays."""
+    heads, g, k3, qb, kb, topk = 2, (1, 8, 16), (6, 16, 30), (1, 8, 16), (1, 4, 8), 80
+    Lk = k3[0] * k3[1] * k3[2]
+    assert B().op_attention_blocks_workspace(1, heads, g, k3, qb, kb, topk) > 0
+    q, k, v = rnd((1, 128, heads * 128), 151), rnd((1, Lk, heads * 128), 152), rnd((1, Lk, heads * 128), 153)
+
+    def both():
+        blocks, counts = B().op_block_select(q, k, heads, g, k3, qb, kb, topk)
+        return blocks, B().op_attention_blocks(q, k, v, heads, g, k3, qb, kb, blocks, counts)
+
+    both()
+    B().op_sync()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = both()
+    for seed in (154, 155):
+        for i, x in enumerate((q, k, v)):
+            x.copy_(rnd(x.shape, 10 * seed + i))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = both()
+        B().op_sync()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_streams_given_by_handle():
+    heads, page, per, T = 2, 32, 50, 3
+    kc, vc, table = cache(2, per, page, heads, 161)
+    q = rnd((2, T, heads * 128), 162)
+    ln = torch.tensor([1500, 40], dtype=torch.int32, device="cuda")
+    want = B().op_attention_paged(q, kc, vc, table, ln, heads)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream):
+        out = B().op_attention_paged(q, kc, vc, table, ln, heads, stream=stream)
+        s.synchronize()
+        assert torch.equal(out, want)
+    assert torch.cuda.current_stream() != s

@@ -519,6 +519,8 @@ class _BlockPlan:
             for g, b in zip(grid, block):
                 n *= -(-g // b) if b > 0 else 0
             return n
+        if any(len(d) != 3 for d in (q_grid, k_grid, q_block, k_block)):
+            raise ValueError("grids and blocks are (frames, rows, columns)")
         self.grid = _block_grid(q_grid, k_grid, q_block, k_block)
         self.ref = C.byref(self.grid)
         self.Lq, self.Lk = (g[0] * g[1] * g[2] for g in (q_grid, k_grid))
@@ -557,6 +559,8 @@ class _on:
         if stream is not None or device.index != torch.cuda.current_device():
             self.enter = [torch.cuda.device(device)]
             if stream is not None:
+                if not isinstance(stream, int) and stream.device != device:
+                    raise ValueError(f"stream: a stream of {device} is needed, got one of {stream.device}")
                 s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
                 self.enter.append(torch.cuda.stream(s))
 

@@ -1418,6 +1418,8 @@ bool aligned16(std::initializer_list<const void*> ptrs) {
 
 bool ld_ok(int64_t ld, int heads) { return ld >= 128ll * heads && ld % 8 == 0 && ld < (1ll << 31); }
 
+constexpr int MAX_LIST = 1 << 24;  // entries of a list of key blocks (times two groups each, still an int)
+
 bool group_ok(int64_t n) { return n == 16 || n == 32 || n == 64 || n == 128; }
 
 // Sizes of a block grid within the limits (B, heads included); fills *out.
@@ -1469,7 +1471,7 @@ wan_status wan_op_block_select(const void* q, int64_t ldq, const void* k, int64_
 
 int64_t wan_op_attention_blocks_workspace(int B, int heads, const wan_block_grid* g, int topk) {
     wan::BlockGrid bg;
-    if (!g || topk < 1 || !block_grid_ok(g, B, heads, &bg)) return -1;
+    if (!g || topk < 1 || topk > MAX_LIST || !block_grid_ok(g, B, heads, &bg)) return -1;
     return wan::attention_blocks_workspace(B, heads, bg, topk);
 }
 
@@ -1479,7 +1481,7 @@ wan_status wan_op_attention_blocks(const void* q, int64_t ldq, const void* k, in
                                    void* stream) {
     if (!q || !k || !v || !o || !g || !blocks || !counts) return WAN_EINVAL;
     wan::BlockGrid bg;
-    if (topk < 1 || !block_grid_ok(g, B, heads, &bg)) return WAN_ESHAPE;
+    if (topk < 1 || topk > MAX_LIST || !block_grid_ok(g, B, heads, &bg)) return WAN_ESHAPE;
     if (!ld_ok(ldq, heads) || !ld_ok(ldk, heads) || !ld_ok(ldv, heads) || !ld_ok(ldo, heads) ||
         !aligned16({q, k, v, o, workspace}))
         return WAN_ESHAPE;
