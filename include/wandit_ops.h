@@ -207,7 +207,7 @@ typedef struct {
  * are zeroed if zero_rest != 0 (for a buffer that is not q itself) or left.  Two
  * sequences that share a page must not write the same place.
  * Errors before any launch: WAN_EINVAL for a null pointer, WAN_ESHAPE for B, T <
- * 0, B * T > 2^31, heads outside [1, 96], a RoPE split that is not even with sum
+ * 0, B * T > 2^29, heads outside [1, 96], a RoPE split that is not even with sum
  * 128, H, W <= 0, H * W > 2^30, theta <= 0, strides or pointers (k, v, q, q_out,
  * the cache, gains) that are not 16-byte aligned, a leading dimension or token
  * stride below 128 * heads, a page stride that lets pages overlap, or a cache

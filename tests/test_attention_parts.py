@@ -177,3 +177,10 @@ def test_python_wrappers_refuse_grids_and_streams_that_do_not_fit(lib):
             binding.op_block_select_workspace(1, 2, *d)
     with pytest.raises(ValueError, match="stream of cuda:0"):
         binding._on(torch.device("cuda", 0), types.SimpleNamespace(device=torch.device("cuda", 1)))
+
+
+def test_append_refuses_more_rows_than_its_grid_holds(lib):
+    c = cache()
+    for B, T in ((1, (1 << 29) + 1), (1 << 15, 1 << 15)):
+        assert lib.wan_op_kv_append(FAKE, 256, FAKE, 256, B, T, 2, FAKE, None, None, 1e-6, 0, 0, 0, 0, 0, 0, 1e4, None, 0, None,
+                                    None, 0, 0, C.byref(c), None) == ESHAPE

@@ -73,15 +73,6 @@ constexpr int PLAN_SMS = 148;              // SMs the split plan assumes
 enum Mode { BLOCKS, PAGES };
 }  // namespace alist
 
-// n / d for n < 2^31 by a multiplication: the producers decode block numbers, and
-// a division is a long dependent sequence for a warp that shares its scheduler.
-struct FastDiv {
-    uint32_t mul, shift;
-    __device__ __forceinline__ int operator()(int n) const {
-        return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift);
-    }
-};
-
 struct ListParams {
     int units, splits, nqb, heads, B;
     int rows;               // rows of a full query tile
@@ -910,12 +901,6 @@ int log2_of(int v) {
     int n = 0;
     while ((1 << n) < v) ++n;
     return n;
-}
-
-FastDiv fast_div(int d) {
-    const uint32_t shift = (uint32_t)log2_of(d);
-    const uint64_t mul = ((1ull << 32) * ((1ull << shift) - (uint64_t)d)) / (uint64_t)d + 1;
-    return FastDiv{(uint32_t)mul, shift};
 }
 
 // Token groups of a block or page of `tokens` (16, 32, 64 or 128) tokens.

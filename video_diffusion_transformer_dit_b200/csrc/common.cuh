@@ -555,4 +555,18 @@ __device__ __forceinline__ float2 unpack_bf16(uint32_t u) {
     return __bfloat1622float2(h);
 }
 
+// n / d for n < 2^31 by a multiplication: a division is a long dependent sequence.
+struct FastDiv {
+    uint32_t mul, shift;
+    __device__ __forceinline__ int operator()(int n) const {
+        return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift);
+    }
+};
+inline FastDiv fast_div(int d) {
+    uint32_t shift = 0;
+    while ((1ll << shift) < d) ++shift;
+    const uint64_t mul = ((1ull << 32) * ((1ull << shift) - (uint64_t)d)) / (uint64_t)d + 1;
+    return FastDiv{(uint32_t)mul, shift};
+}
+
 }  // namespace wan

@@ -1503,7 +1503,7 @@ wan_status wan_op_kv_append(const void* k, int64_t ldk, const void* v, int64_t l
                             void* stream) {
     if (!k || !v || !start || !cache || !cache->k || !cache->v || !cache->table || (q && !q_out)) return WAN_EINVAL;
     wan::KvPages pages;
-    if (B < 0 || T < 0 || heads <= 0 || heads > 96 || (int64_t)B * T > (1ll << 31) || !kv_cache_ok(cache, heads, &pages))
+    if (B < 0 || T < 0 || heads <= 0 || heads > 96 || (int64_t)B * T > (1ll << 29) || !kv_cache_ok(cache, heads, &pages))
         return WAN_ESHAPE;
     if (!ld_ok(ldk, heads) || !ld_ok(ldv, heads) || (q && (!ld_ok(ldq, heads) || !ld_ok(ldqo, heads)))) return WAN_ESHAPE;
     if (!aligned16({k, v, q, q ? q_out : nullptr, k_gain, q_gain})) return WAN_ESHAPE;
