@@ -176,7 +176,8 @@ def test_python_wrappers_refuse_grids_and_streams_that_do_not_fit(lib):
         with pytest.raises(ValueError, match="frames, rows, columns"):
             binding.op_block_select_workspace(1, 2, *d)
     with pytest.raises(ValueError, match="stream of cuda:0"):
-        binding._on(torch.device("cuda", 0), types.SimpleNamespace(device=torch.device("cuda", 1)))
+        binding._torch()
+        binding._elsewhere(torch.device("cuda", 0), types.SimpleNamespace(device=torch.device("cuda", 1)))
 
 
 def test_append_refuses_more_rows_than_its_grid_holds(lib):

@@ -485,15 +485,28 @@ def op_attention_ptr(q, ldq, k, ldk, v, ldv, o, ldo, B, heads, Lq, Lk, stream=No
 
 # ---------------------------------------------------------------- attention over parts of the sequence
 # These calls are made per layer and per token, where the host's time counts: sizes that follow
-# from the geometry alone are worked out once per geometry (lru_cache), tensors are looked at once.
+# from the geometry alone are worked out once per geometry (lru_cache), tensors are looked at once,
+# and only a call for another device or stream than the current ones enters a context.
+_th = None          # torch
+_raw_stream = None  # handle of a device's current stream (torch's own short way to it where there is one)
+
+
+def _torch():
+    global _th, _raw_stream
+    if _th is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _th = torch
+    return _th
+
+
 def _rows(name, t, B, L, D, device) -> int:
     """Leading dimension of a bf16 tensor [B, L, D] whose row (b, l) lies at (b * L + l) * ld."""
-    import torch
-    shape, st = t.shape, t.stride()
-    if t.dtype is not torch.bfloat16 or len(shape) != 3 or shape[0] != B or shape[1] != L or shape[2] != D or \
-            t.device != device or device.type != "cuda":
+    st = t.stride()
+    if t.dtype is not _th.bfloat16 or t.shape != (B, L, D) or t.device != device:
         raise ValueError(f"{name}: a bf16 CUDA tensor [{B}, {L}, {D}] on {device} is needed, "
-                         f"got {tuple(shape)} {t.dtype} on {t.device}")
+                         f"got {tuple(t.shape)} {t.dtype} on {t.device}")
     ld = st[1] if L > 1 else st[0] if B > 1 and L == 1 else D
     if st[2] != 1 or (B > 1 and L > 1 and st[0] != L * ld):
         raise ValueError(f"{name}: rows must be dense and samples follow each other, got strides {st}")
@@ -541,46 +554,26 @@ def _paged_bytes(B, heads, T, page_stride, token_stride, num_pages, page_size, t
     return lib().wan_op_attention_paged_workspace(B, heads, T, C.byref(c))
 
 
-def _current_raw_stream(index: int) -> int:
-    """Handle of the device's current stream (torch's own short way to it where there is one)."""
-    import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
-
-
-class _on:
-    """The tensors' device and the launch stream made current for a call: buffers that the call allocates
-    belong to the stream that uses them.  Gives the stream's handle."""
-    __slots__ = ("device", "enter")
-
-    def __init__(self, device, stream):
-        import torch
-        self.device, self.enter = device, ()
-        if stream is not None or device.index != torch.cuda.current_device():
-            self.enter = [torch.cuda.device(device)]
-            if stream is not None:
-                if not isinstance(stream, int) and stream.device != device:
-                    raise ValueError(f"stream: a stream of {device} is needed, got one of {stream.device}")
-                s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
-                self.enter.append(torch.cuda.stream(s))
-
-    def __enter__(self):
-        for c in self.enter:
-            c.__enter__()
-        return _current_raw_stream(self.device.index)
-
-    def __exit__(self, *exc):
-        for c in reversed(self.enter):
-            c.__exit__(*exc)
+def _elsewhere(device, stream):
+    """None where a call for tensors on `device` runs on the current device and stream, else a context that makes
+    theirs current: buffers that the call allocates belong to the stream that uses them."""
+    if device.type != "cuda":
+        raise ValueError(f"tensors on a CUDA device are needed, got {device}")
+    if stream is None:
+        return None if device.index == _th.cuda.current_device() else _th.cuda.device(device)
+    if isinstance(stream, int):
+        stream = _th.cuda.ExternalStream(stream, device=device)
+    elif stream.device != device:
+        raise ValueError(f"stream: a stream of {device} is needed, got one of {stream.device}")
+    return _th.cuda.stream(stream)
 
 
 def _scratch(nbytes, given, device):
     """(pointer, bytes, tensor) of the caller's workspace or of a new one."""
-    import torch
     if given is None:
         if nbytes <= 0:
             return None, 0, None
-        given = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        given = _th.empty(nbytes, dtype=_th.uint8, device=device)
         return given.data_ptr(), nbytes, given
     if given.device != device or not given.is_contiguous():
         raise ValueError(f"workspace: a contiguous tensor on {device} is needed, got one on {given.device}")
@@ -597,26 +590,30 @@ def op_block_select(q, k, heads, q_grid, k_grid, q_block, k_block, topk, mask=No
     slices of a packed projection will do), grids and blocks (frames, rows, columns), mask uint8 [query blocks,
     key blocks] or None.  Returns (blocks int32 [B, heads, query blocks, topk], counts int32 [B, heads, query
     blocks]).  Buffers that are not given are allocated."""
-    import torch
-    B, dev = q.shape[0], q.device
+    torch, dev = _torch(), q.device
+    other = _elsewhere(dev, stream)
+    if other is not None:
+        with other:
+            return op_block_select(q, k, heads, q_grid, k_grid, q_block, k_block, topk, mask, blocks, counts, workspace)
+    B = q.shape[0]
     p = _block_plan(B, heads, tuple(q_grid), tuple(k_grid), tuple(q_block), tuple(k_block), topk)
     ldq, ldk = _rows("q", q, B, p.Lq, heads * 128, dev), _rows("k", k, B, p.Lk, heads * 128, dev)
     if mask is not None:
         _dense("mask", mask, (p.nq, p.nk), torch.uint8, dev)
-    with _on(dev, stream) as st:
-        if blocks is None:
-            blocks = torch.empty((B, heads, p.nq, max(topk, 0)), dtype=torch.int32, device=dev)
-        else:
-            _dense("blocks", blocks, (B, heads, p.nq, topk), torch.int32, dev)
-        if counts is None:
-            counts = torch.empty((B, heads, p.nq), dtype=torch.int32, device=dev)
-        else:
-            _dense("counts", counts, (B, heads, p.nq), torch.int32, dev)
-        if B == 0:
-            return blocks, counts
-        ws, nbytes, _keep = _scratch(p.select_bytes, workspace, dev)
-        _check(lib().wan_op_block_select(q.data_ptr(), ldq, k.data_ptr(), ldk, B, heads, p.ref, _ptr(mask), topk,
-                                         blocks.data_ptr(), counts.data_ptr(), ws, nbytes, st), "wan_op_block_select")
+    if blocks is None:
+        blocks = torch.empty((B, heads, p.nq, max(topk, 0)), dtype=torch.int32, device=dev)
+    else:
+        _dense("blocks", blocks, (B, heads, p.nq, topk), torch.int32, dev)
+    if counts is None:
+        counts = torch.empty((B, heads, p.nq), dtype=torch.int32, device=dev)
+    else:
+        _dense("counts", counts, (B, heads, p.nq), torch.int32, dev)
+    if B == 0:
+        return blocks, counts
+    ws, nbytes, _keep = _scratch(p.select_bytes, workspace, dev)
+    _check(lib().wan_op_block_select(q.data_ptr(), ldq, k.data_ptr(), ldk, B, heads, p.ref, _ptr(mask), topk,
+                                     blocks.data_ptr(), counts.data_ptr(), ws, nbytes, _raw_stream(dev.index)),
+           "wan_op_block_select")
     return blocks, counts
 
 
@@ -629,39 +626,39 @@ def op_attention_blocks(q, k, v, heads, q_grid, k_grid, q_block, k_block, blocks
     """Attention of each query block over its listed key blocks (wan_op_attention_blocks): q, k, v bf16 [B, L, D],
     blocks int32 [B, heads, query blocks, topk], counts int32 [B, heads, query blocks]; lse f32 [B, heads, query
     tokens] is filled if given.  Returns out, bf16 [B, query tokens, D]."""
-    import torch
-    B, topk, dev, D = q.shape[0], blocks.shape[-1], q.device, heads * 128
+    torch, dev = _torch(), q.device
+    other = _elsewhere(dev, stream)
+    if other is not None:
+        with other:
+            return op_attention_blocks(q, k, v, heads, q_grid, k_grid, q_block, k_block, blocks, counts, out, lse, workspace)
+    B, topk, D = q.shape[0], blocks.shape[-1], heads * 128
     p = _block_plan(B, heads, tuple(q_grid), tuple(k_grid), tuple(q_block), tuple(k_block), topk)
     ldq, ldk, ldv = _rows("q", q, B, p.Lq, D, dev), _rows("k", k, B, p.Lk, D, dev), _rows("v", v, B, p.Lk, D, dev)
     _dense("blocks", blocks, (B, heads, p.nq, topk), torch.int32, dev)
     _dense("counts", counts, (B, heads, p.nq), torch.int32, dev)
     if lse is not None:
         _dense("lse", lse, (B, heads, p.Lq), torch.float32, dev)
-    with _on(dev, stream) as st:
-        if out is None:
-            out = torch.empty((B, p.Lq, D), dtype=torch.bfloat16, device=dev)
-            ldo = D
-        else:
-            ldo = _rows("out", out, B, p.Lq, D, dev)
-        if B == 0:
-            return out
-        ws, nbytes, _keep = _scratch(p.attend_bytes, workspace, dev)
-        _check(lib().wan_op_attention_blocks(q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, out.data_ptr(), ldo, B,
-                                             heads, p.ref, blocks.data_ptr(), counts.data_ptr(), topk, _ptr(lse), ws, nbytes,
-                                             st), "wan_op_attention_blocks")
+    if out is None:
+        out, ldo = q.new_empty((B, p.Lq, D)), D
+    else:
+        ldo = _rows("out", out, B, p.Lq, D, dev)
+    if B == 0:
+        return out
+    ws, nbytes, _keep = _scratch(p.attend_bytes, workspace, dev)
+    _check(lib().wan_op_attention_blocks(q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, out.data_ptr(), ldo, B,
+                                         heads, p.ref, blocks.data_ptr(), counts.data_ptr(), topk, _ptr(lse), ws, nbytes,
+                                         _raw_stream(dev.index)), "wan_op_attention_blocks")
     return out
 
 
 def _kv_cache(k_cache, v_cache, table, B, D, device) -> wan_kv_cache:
-    import torch
-    shape, st = k_cache.shape, k_cache.stride()
-    if k_cache.dtype is not torch.bfloat16 or v_cache.dtype is not torch.bfloat16 or len(shape) != 3 or shape[2] != D or \
-            st[2] != 1 or v_cache.shape != shape or v_cache.stride() != st or k_cache.device != device or \
-            v_cache.device != device or device.type != "cuda":
+    shape, st, bf16 = k_cache.shape, k_cache.stride(), _th.bfloat16
+    if k_cache.dtype is not bf16 or v_cache.dtype is not bf16 or len(shape) != 3 or shape[2] != D or st[2] != 1 or \
+            v_cache.shape != shape or v_cache.stride() != st or k_cache.device != device or v_cache.device != device:
         raise ValueError(f"k_cache, v_cache: bf16 tensors [pages, page size, {D}] of one layout with dense rows on {device} "
                          f"are needed, got {tuple(shape)} and {tuple(v_cache.shape)}, strides {st} and {v_cache.stride()}")
     ts, tst = table.shape, table.stride()
-    if len(ts) != 2 or table.dtype is not torch.int32 or (ts[1] > 1 and tst[1] != 1) or ts[0] != B or table.device != device:
+    if len(ts) != 2 or table.dtype is not _th.int32 or (ts[1] > 1 and tst[1] != 1) or ts[0] != B or table.device != device:
         raise ValueError(f"page table: an int32 tensor [{B}, pages] on {device} is needed, "
                          f"got {tuple(ts)} {table.dtype} on {table.device}")
     return wan_kv_cache(k_cache.data_ptr(), v_cache.data_ptr(), st[0] if shape[0] > 1 else shape[1] * st[1],
@@ -675,9 +672,14 @@ def op_kv_append(k, v, k_cache, v_cache, table, start, heads, frame, count=None,
     bf16 [pages, page size, D], table int32 [B, pages], start (and count) int32 [B], frame = (rows, columns) of
     the token grid, gains f32 [D] (None: no norm).  Returns the rotated queries (q_out, by default a new tensor
     whose rows past count are zero) or None without q."""
-    import torch
+    torch, dev = _torch(), k.device
+    other = _elsewhere(dev, stream)
+    if other is not None:
+        with other:
+            return op_kv_append(k, v, k_cache, v_cache, table, start, heads, frame, count, k_gain, q, q_gain, q_out, eps,
+                                rope, split, theta)
     B, T = k.shape[:2]
-    dev, D = k.device, heads * 128
+    D = heads * 128
     ldk, ldv = _rows("k", k, B, T, D, dev), _rows("v", v, B, T, D, dev)
     _dense("start", start, (B,), torch.int32, dev)
     if count is not None:
@@ -688,25 +690,25 @@ def op_kv_append(k, v, k_cache, v_cache, table, start, heads, frame, count=None,
         _dense("q_gain", q_gain, (D,), torch.float32, dev)
     c = _kv_cache(k_cache, v_cache, table, B, D, dev)
     ldq = ldqo = fresh = 0
-    with _on(dev, stream) as st:
-        if q is None:
-            q_out = None
+    if q is None:
+        q_out = None
+    else:
+        ldq = _rows("q", q, B, T, D, dev)
+        if q_out is None:
+            q_out, ldqo, fresh = q.new_empty((B, T, D)), D, 1
         else:
-            ldq = _rows("q", q, B, T, D, dev)
-            if q_out is None:
-                q_out, ldqo, fresh = torch.empty((B, T, D), dtype=torch.bfloat16, device=dev), D, 1
-            else:
-                ldqo = _rows("q_out", q_out, B, T, D, dev)
-        if B == 0 or T == 0:
-            return q_out
-        _check(lib().wan_op_kv_append(k.data_ptr(), ldk, v.data_ptr(), ldv, B, T, heads, start.data_ptr(), _ptr(count),
-                                      _ptr(k_gain), eps, 1 if rope else 0, frame[0], frame[1], split[0], split[1], split[2],
-                                      theta, _ptr(q), ldq, _ptr(q_gain), _ptr(q_out), ldqo, fresh, C.byref(c), st),
-               "wan_op_kv_append")
+            ldqo = _rows("q_out", q_out, B, T, D, dev)
+    if B == 0 or T == 0:
+        return q_out
+    _check(lib().wan_op_kv_append(k.data_ptr(), ldk, v.data_ptr(), ldv, B, T, heads, start.data_ptr(), _ptr(count),
+                                  _ptr(k_gain), eps, 1 if rope else 0, frame[0], frame[1], split[0], split[1], split[2],
+                                  theta, _ptr(q), ldq, _ptr(q_gain), _ptr(q_out), ldqo, fresh, C.byref(c),
+                                  _raw_stream(dev.index)), "wan_op_kv_append")
     return q_out
 
 
 def op_attention_paged_workspace(B, heads, T, k_cache, v_cache, table) -> int:
+    _torch()
     c = _kv_cache(k_cache, v_cache, table, B, heads * 128, k_cache.device)
     return lib().wan_op_attention_paged_workspace(B, heads, T, C.byref(c))
 
@@ -715,26 +717,28 @@ def op_attention_paged(q, k_cache, v_cache, table, lens, heads, out=None, lse=No
     """Attention of T new tokens per sequence over its cached places [0, lens[b]) (wan_op_attention_paged): q bf16
     [B, T, D], caches bf16 [pages, page size, D], table int32 [B, pages], lens int32 [B]; lse f32 [B, heads, T] is
     filled if given.  Returns out, bf16 [B, T, D]."""
-    import torch
+    torch, dev = _torch(), q.device
+    other = _elsewhere(dev, stream)
+    if other is not None:
+        with other:
+            return op_attention_paged(q, k_cache, v_cache, table, lens, heads, out, lse, workspace)
     B, T = q.shape[:2]
-    dev, D = q.device, heads * 128
+    D = heads * 128
     ldq = _rows("q", q, B, T, D, dev)
     c = _kv_cache(k_cache, v_cache, table, B, D, dev)
     _dense("lens", lens, (B,), torch.int32, dev)
     if lse is not None:
         _dense("lse", lse, (B, heads, T), torch.float32, dev)
-    with _on(dev, stream) as st:
-        if out is None:
-            out = torch.empty((B, T, D), dtype=torch.bfloat16, device=dev)
-            ldo = D
-        else:
-            ldo = _rows("out", out, B, T, D, dev)
-        if B == 0 or T == 0:
-            return out
-        need = _paged_bytes(B, heads, T, c.page_stride, c.token_stride, c.num_pages, c.page_size, c.table_ld, c.max_pages)
-        ws, nbytes, _keep = _scratch(need, workspace, dev)
-        _check(lib().wan_op_attention_paged(q.data_ptr(), ldq, C.byref(c), lens.data_ptr(), out.data_ptr(), ldo, B, heads, T,
-                                            _ptr(lse), ws, nbytes, st), "wan_op_attention_paged")
+    if out is None:
+        out, ldo = q.new_empty((B, T, D)), D
+    else:
+        ldo = _rows("out", out, B, T, D, dev)
+    if B == 0 or T == 0:
+        return out
+    need = _paged_bytes(B, heads, T, c.page_stride, c.token_stride, c.num_pages, c.page_size, c.table_ld, c.max_pages)
+    ws, nbytes, _keep = _scratch(need, workspace, dev)
+    _check(lib().wan_op_attention_paged(q.data_ptr(), ldq, C.byref(c), lens.data_ptr(), out.data_ptr(), ldo, B, heads, T,
+                                        _ptr(lse), ws, nbytes, _raw_stream(dev.index)), "wan_op_attention_paged")
     return out
 
 
