@@ -17,9 +17,19 @@
 //                       so of several hundred) are scored again, in fp64, and
 //                       ranked by that.
 // (With hi + lo parts and three products fewer are scored again, but the products
-// and their operands cost more than that saves: 30 against 12 us of the pair's.)
+// and their operands cost more than that saves: 30 against 14 us of the pair's.)
 // Longer rows: block_score64_kernel and block_topk64_kernel, all in fp64.
+//
+// Measured, us: means 75 (5.4 TB/s), scores 14, top-k 28 of the 480p pair (B = 2, 12
+// heads, 32760 tokens, 336 x 624 blocks); 248 (6.3 TB/s), 44 and 93 with 40 heads, 75600
+// tokens, 720 x 720 blocks and a mask.  The means are bound by memory; the scores by
+// their way through the L2, and 64 x 128 tiles, which read a quarter less, take 2 us off
+// the 44; the top-k by instruction issue (65 %): 2300 per row of 720.  Starting each kernel
+// while the one before it drains costs the large cases more (1 %) than it saves.
 #include <cuda_fp16.h>
+
+#include <cfloat>
+#include <climits>
 
 #include <type_traits>
 
@@ -41,14 +51,14 @@ constexpr float SCORE_TINY = 1e-36f;            // below it scores lose bits to 
 
 // Means of the blocks of q (first g.q_blocks() CTAs) and k, per head: fp64, fp16 of
 // unit length, and norm (NaN or infinite where a mean is).  One CTA per block and
-// column slice, eight columns per thread, four tokens loaded while the four before
-// are added; where there are few CTAs (a small grid) RG = 4 groups of threads take
-// every fourth eight tokens each: a block is a chain of loads (14.5 -> 7.6 us at 15
-// blocks).  Every token is added in fp64: it must not matter what stands beside a
-// small one.  (Sums of four tokens in fp32 first, which lose a value 2^17 times
-// smaller than its neighbour, took 70 us where this takes 72; the same with the
-// rounding errors kept beside them 133.)  The conversions to fp64, at 16 a clock and
-// SM, are two thirds busy then; the loads are what bounds it.
+// column slice, eight columns per thread, four tokens loaded (evict-first: nothing
+// reads them again here; 6 us of the pair's 81) while the four before are added; where
+// there are few CTAs (a small grid) RG = 4 groups of threads take every fourth eight
+// tokens each: a block is a chain of loads (14.5 -> 7.6 us at 15 blocks).  Every token
+// is added in fp64: it must not matter what stands beside a small one.  (Sums of
+// four tokens in fp32 first, which lose a value 2^17 times smaller than its
+// neighbour, take 2 us less of the pair's; the same with the rounding errors
+// kept beside them 60 more.)
 struct MeanOut {
     double* mean;           // [B, heads, blocks, 128]
     __half* unit;           // [B, heads, blocks, 128], null: not wanted
@@ -97,7 +107,7 @@ __global__ void __launch_bounds__(256) block_mean_kernel(const __nv_bfloat16* __
     auto fetch = [&](int t, uint4 (&v)[4]) {
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-            v[u] = t + u < n ? __ldg(reinterpret_cast<const uint4*>(base + (long long)tokens[t + u] * ld)) : make_uint4(0, 0, 0, 0);
+            v[u] = t + u < n ? __ldcs(reinterpret_cast<const uint4*>(base + (long long)tokens[t + u] * ld)) : make_uint4(0, 0, 0, 0);
     };
     if (RG == 1) {
         uint4 a[4], b[4];  // past the end fetch() gives zeros
@@ -174,7 +184,7 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
 }
 
 // scores[bh][i][j] = (unit mean of q block i) . (unit mean of k block j) * |k j|,
-// rows `pitch` apart.  64 x 64 scores per CTA, four warps of 32 x 32; both operands
+// rows `pitch` apart and filled up with -inf.  64 x 64 scores per CTA, four warps of 32 x 32; both operands
 // whole (K = 128) in shared memory, 256 bytes a row, 16-byte pieces swizzled by the
 // row.  mma.sync and not tcgen05: a few microseconds of work, in tiles too small
 // for a 128-row accumulator.
@@ -222,8 +232,8 @@ __global__ void __launch_bounds__(128) block_score_kernel(const __half* __restri
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int col = k0 + n0 + 8 * j + (lane & 3) * 2;  // even, as the pitch is
-        if (col >= nk) continue;
-        const float s0 = __ldg(kn + bh * pitch + col), s1 = col + 1 < nk ? __ldg(kn + bh * pitch + col + 1) : 0.f;
+        if (col >= pitch) continue;
+        const float s0 = col < nk ? __ldg(kn + bh * pitch + col) : 0.f, s1 = col + 1 < nk ? __ldg(kn + bh * pitch + col + 1) : 0.f;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -231,7 +241,8 @@ __global__ void __launch_bounds__(128) block_score_kernel(const __half* __restri
                 const int row = q0 + m0 + 16 * i + half * 8 + (lane >> 2);
                 if (row < nq)
                     *reinterpret_cast<float2*>(scores + (bh * nq + row) * pitch + col) =
-                        make_float2(acc[i][j][half * 2] * s0, acc[i][j][half * 2 + 1] * s1);
+                        make_float2(col < nk ? acc[i][j][half * 2] * s0 : -INFINITY,
+                                    col + 1 < nk ? acc[i][j][half * 2 + 1] * s1 : -INFINITY);
             }
     }
 }
@@ -312,14 +323,17 @@ __global__ void __launch_bounds__(128) block_score64_kernel(const double* __rest
     }
 }
 
-// The topk best blocks of a row: one warp per row, a lane holding the keys of NPL
-// consecutive blocks in registers (nk <= 32 NPL).  A threshold that leaves topk
-// keys is found by interpolation and bisection in turn (half a dozen counts).
-// With a_j the fp32 score of block j and d_j the bound of its error, the topk-th
-// best 64-bit score is at least L = min (a_j - d_j) over the topk best a_j and at
-// most U = max (a_j + d_j) over the topk-th and all others: blocks with a_j - d_j >
-// U are taken, those with a_j + d_j < L are not, and the close ones in between are
-// ranked by their fp64 scores, equal ones to the lower block.
+// The topk best blocks of a row: one warp per row, a lane holding the scores of NPL
+// consecutive blocks in registers (nk <= 32 NPL).  A threshold `at` that leaves
+// topk scores is found by interpolation (half a dozen counts).  With d the bound of
+// all scores' errors, topk blocks have 64-bit scores of at - d or more, and the blocks
+// below the threshold less than at + d: a block whose score lies more than 2 d above
+// the threshold is taken, one more than 2 d below is not, and the close ones in
+// between (twenty or so of several hundred, where blocks of fewer tokens at the
+// grid's edge have longer means), one per lane, are narrowed by their own bounds d_j:
+// taken is a_j - d_j > U = max (a_j + d_j) over the topk-th best score and all below
+// it, left is a_j + d_j < L = min (a_j - d_j) over the topk best.  What remains (seven
+// or so) is ranked by its fp64 scores, equal ones to the lower block.
 struct TopkParams {
     const float* scores;            // [B heads nq, pitch]
     const double *qm, *km;          // means
@@ -329,55 +343,97 @@ struct TopkParams {
     int nq, nk, pitch, topk;
     int *blocks, *counts;
 };
+// Up to 24 scores per lane seven CTAs share an SM, at 72 registers (eight, at 64, spill: 117
+// against 114 us for the pair's three kernels; six: 118).  NPL is the next of a few sizes:
+// the scans are unrolled over it, so their cost is NPL's, not the row's.
 template <int NPL>
-__global__ void __launch_bounds__(128, NPL <= 24 ? 8 : 1) block_topk_kernel(const __grid_constant__ TopkParams p) {
+__global__ void __launch_bounds__(128, NPL <= 24 ? 7 : 1) block_topk_kernel(const __grid_constant__ TopkParams p) {
     using Bits = typename std::conditional<(NPL > 32), unsigned long long, uint32_t>::type;
     // rows come in coalesced and are read back a lane's consecutive blocks at a time
     __shared__ int again[4][32];
-    __shared__ float4 norms[NPL * 8], stage[4][NPL * 8];
+    __shared__ uint32_t longest[4];
+    __shared__ float4 stage[4][NPL * 8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int nk = p.nk, j0 = lane * NPL;  // the lane's first block
     const long long bh = blockIdx.y;
     const int i_q = blockIdx.x * 4 + warp;
     const long long row = bh * p.nq + i_q;
-    bool number = true;  // every norm of the head is one
-    for (int i = threadIdx.x; i < NPL * 8; i += 128) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i < p.pitch / 4) {
-            v = __ldg(reinterpret_cast<const float4*>(p.kn + bh * p.pitch) + i);
-            const int rest = nk - 4 * i;
-            number = number && v.x < INFINITY && (rest < 2 || v.y < INFINITY) && (rest < 3 || v.z < INFINITY) &&
-                     (rest < 4 || v.w < INFINITY);
-        }
-        norms[i] = v;
-    }
+    const float* kn = p.kn + bh * p.pitch;
+    uint32_t most = 0;  // the head's longest key, as bits: NaN above infinity above all numbers
+    for (int i = threadIdx.x; i < nk; i += 128) most = max(most, __float_as_uint(__ldg(kn + i)) & 0x7fffffffu);
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) longest[warp] = most;
     if (i_q < p.nq) {
         const float4* src = reinterpret_cast<const float4*>(p.scores + row * p.pitch);
 #pragma unroll
         for (int i = 0; i < NPL / 4; ++i)
-            if (i * 32 + lane < p.pitch / 4) stage[warp][i * 32 + lane] = __ldg(src + i * 32 + lane);
+            stage[warp][i * 32 + lane] = i * 32 + lane < p.pitch / 4
+                                             ? __ldg(src + i * 32 + lane)
+                                             : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
     }
-    number = __syncthreads_and(number);
+    __syncthreads();
     if (i_q >= p.nq) return;
-    // scores of the allowed blocks; NaN, which no comparison holds for, where there is none or
-    // it is not the score that decides: `extra` are the blocks asked for
+    const float key_norm = __uint_as_float(max(max(longest[0], longest[1]), max(longest[2], longest[3])));
+    const bool number = key_norm < 1e38f && p.qn[row] < INFINITY;  // every score is one
+    // scores, -inf where there is no block or it is not the score that decides: `extra` are the
+    // blocks asked for, `allowed` those left to their scores
     float f[NPL];
-    Bits extra = 0;
 #pragma unroll
     for (int i = 0; i < NPL; i += 4) {
         const float4 v = stage[warp][(j0 + i) / 4];
-        const float x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) f[i + c] = j0 + i + c < nk ? (x[c] == x[c] ? x[c] : -INFINITY) : NAN;
+        f[i] = v.x;
+        f[i + 1] = v.y;
+        f[i + 2] = v.z;
+        f[i + 3] = v.w;
     }
-    if (p.mask) {
-        const uint8_t* mrow = p.mask + (long long)i_q * nk + j0;
+    // their mean and spread, from the lanes that are full (before the mask: a guess)
+    float sum = 0.f, sum2 = 0.f;
+    {
+        uint64_t a = 0ull, b = 0ull;
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) {
-            const uint8_t m = j0 + i < nk ? __ldg(mrow + i) : 0;
-            f[i] = m == 1 ? f[i] : NAN;
-            extra |= (Bits)(m > 1) << i;
+        for (int i = 0; i < NPL; i += 2) {
+            const uint64_t x = f2pack(f[i], f[i + 1]);
+            a = add2(a, x);
+            b = fma2(x, x, b);
         }
+        float x, y;
+        f2unpack(a, x, y);
+        sum = x + y;
+        f2unpack(b, x, y);
+        sum2 = x + y;
+    }
+    const bool full = fabsf(sum) < INFINITY && sum2 < INFINITY;
+    const float seen = NPL * __popc(__ballot_sync(0xffffffffu, full));
+    if (!full) sum = sum2 = 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        sum2 += __shfl_xor_sync(0xffffffffu, sum2, o);
+    }
+    const int here = min(max(nk - j0, 0), NPL);
+    Bits allowed = here == 0 ? Bits(0) : ~Bits(0) >> (sizeof(Bits) * 8 - here), extra = 0;
+    if (p.mask) {
+        // the lane's bytes as words, shifted into place; a word is read if a byte of the row is in it
+        const uintptr_t first = reinterpret_cast<uintptr_t>(p.mask) + (long long)i_q * nk + j0;
+        const uintptr_t end = reinterpret_cast<uintptr_t>(p.mask) + ((long long)i_q + 1) * nk;
+        const uint32_t* words = reinterpret_cast<const uint32_t*>(first & ~uintptr_t(3));
+        const uint32_t shift = (uint32_t)(first & 3) * 8;
+        Bits by_score = 0;
+        uint32_t low = first < end ? __ldg(words) : 0u;
+#pragma unroll
+        for (int i = 0; i < NPL; i += 4) {
+            const uint32_t high = reinterpret_cast<uintptr_t>(words + i / 4 + 1) < end ? __ldg(words + i / 4 + 1) : 0u;
+            const uint32_t m = __funnelshift_r(low, high, shift);
+            low = high;
+            // bytes above 1 and bytes that are 1, each as one bit, gathered by a multiplication
+            const uint32_t z = m & 0xfefefefeu, ahead = ((((z & 0x7f7f7f7fu) + 0x7f7f7f7fu) | z) >> 7) & 0x01010101u;
+            by_score |= (Bits)(((m & ~ahead & 0x01010101u) * 0x01020408u) >> 24 & 15u) << i;
+            extra |= (Bits)((ahead * 0x01020408u) >> 24 & 15u) << i;
+        }
+        extra &= allowed;
+        allowed &= by_score;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) f[i] = allowed >> i & 1 ? f[i] : -INFINITY;
     }
     auto bits_of = [](Bits x) { return NPL > 32 ? __popcll(x) : __popc((uint32_t)x); };
     auto count = [&](float at) {  // scores >= at
@@ -387,7 +443,7 @@ __global__ void __launch_bounds__(128, NPL <= 24 ? 8 : 1) block_topk_kernel(cons
         return (int)__reduce_add_sync(0xffffffffu, n);
     };
     const int always = p.mask ? __reduce_add_sync(0xffffffffu, bits_of(extra)) : 0;
-    const int scored = p.mask ? count(-INFINITY) : nk;
+    const int scored = p.mask ? __reduce_add_sync(0xffffffffu, bits_of(allowed)) : nk;
     const int take = min(p.topk, always + scored);
     const int want = take - always;  // of the scored ones
     int* dst = p.blocks + row * p.topk;
@@ -428,91 +484,79 @@ __global__ void __launch_bounds__(128, NPL <= 24 ? 8 : 1) block_topk_kernel(cons
         return;
     }
     if (want == scored) {  // all that is allowed
-        Bits all = extra;
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) all |= (Bits)(f[i] == f[i]) << i;
-        put(all);
+        put(extra | allowed);
         return;
     }
-    // at: a score that `want` scores reach, and no more unless equal ones lie at the border.  The
-    // first place is where normally distributed scores would have it, the next ones are taken by
-    // the counts, every third half way (five counts for a normal row, ten without the first
-    // guess); where that does not settle it (infinities, scores of many magnitudes) half way
-    // between the scores' bit patterns.
-    float lo = INFINITY, hi = -INFINITY, sum = 0.f, sum2 = 0.f;
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-        lo = fminf(lo, f[i]);
-        hi = fmaxf(hi, f[i]);
-        const float x = f[i] == f[i] ? f[i] : 0.f;
-        sum += x;
-        sum2 = fmaf(x, x, sum2);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-        sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        sum2 += __shfl_xor_sync(0xffffffffu, sum2, o);
-    }
-    const float mean = sum / scored, spread = sqrtf(fmaxf(sum2 / scored - mean * mean, 0.f));
-    const float guess = mean + spread * 0.4073f * log2f((float)(scored - want) / (float)want);  // ln 2 / 1.702
-    float at = lo;
-    int n_at = scored, n_hi = 0;  // n_hi: scores >= the last place that was too high
-    for (int step = 0; n_at != want && lo < hi; ++step) {
-        const float part = step % 3 == 0 ? 0.5f : fminf(fmaxf((float)(n_at - want) / (float)(n_at - n_hi), 0.05f), 0.95f);
-        float mid = step == 0 && guess > lo && guess < hi ? guess : lo + part * (hi - lo);
-        if (step >= 24 || !(mid > lo && mid <= hi)) {
-            const uint32_t a = score_key32(lo), b = score_key32(hi);
-            mid = key32_score(a + ((b - a) >> 1) + 1);
+    Bits sure = extra, close = allowed;  // all are close where a mean is not finite
+    float at = -FLT_MAX;
+    if (number) {
+        // at: a score that `want` scores reach, and no more unless equal ones lie at the border.
+        // The first place is where normally distributed scores would have it, the next is a
+        // step by their density there, and between two that enclose it the counts lead, every
+        // third time half way (five counts for a normal row); where that does not settle it
+        // (scores of many magnitudes) half way between the scores' bit patterns.
+        const float mean = sum / seen, spread = sqrtf(fmaxf(sum2 / seen - mean * mean, 0.f));
+        const float share = (float)want / (float)scored;
+        // the logistic curve of slope 1.702 is near the normal one
+        float mid = mean + spread * 0.4073f * log2f((1.f - share) / share);
+        const float per_count = spread / (1.702f * (float)want * (1.f - share));
+        float lo = -FLT_MAX, hi = FLT_MAX;
+        int n_at = scored, n_hi = 0;  // scores >= lo; >= the last place that was too high
+        for (int step = 0; n_at != want && lo < hi; ++step) {
+            if (step >= 24 || !(mid > lo && mid <= hi)) {
+                const uint32_t a = score_key32(lo), b = score_key32(hi);
+                mid = key32_score(a + ((b - a) >> 1) + 1);
+            }
+            const int n = count(mid);
+            const float tried = mid;
+            if (n >= want) {
+                lo = at = mid;
+                n_at = n;
+            } else {
+                hi = key32_score(score_key32(mid) - 1);  // the next lower float
+                n_hi = n;
+            }
+            if (lo > -FLT_MAX && hi < FLT_MAX)
+                mid = lo + (step % 3 == 2 ? 0.5f : fminf(fmaxf((float)(n_at - want) / (float)(n_at - n_hi), 0.05f), 0.95f)) * (hi - lo);
+            else
+                mid = tried + ((float)(n - want) + (n >= want ? 1.f : -1.f)) * per_count * (float)(1 << min(step, 8));
         }
-        const int n = count(mid);
-        if (n >= want) {
-            lo = at = mid;
-            n_at = n;
-        } else {
-            hi = key32_score(score_key32(mid) - 1);  // the next lower float
-            n_hi = n;
-        }
-    }
-    // L, U and the close ones
-    const float4* kn = norms + j0 / 4;
-    float L = INFINITY, U = -INFINITY, vk = INFINITY;
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) vk = fminf(vk, f[i] >= at ? f[i] : INFINITY);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) vk = fminf(vk, __shfl_xor_sync(0xffffffffu, vk, o));
-    float d[4];
-    auto bounds = [&](int i) {  // of four blocks
-        const float4 v = kn[i / 4];
-        d[0] = fmaf(SCORE_ERROR, v.x, SCORE_TINY);
-        d[1] = fmaf(SCORE_ERROR, v.y, SCORE_TINY);
-        d[2] = fmaf(SCORE_ERROR, v.z, SCORE_TINY);
-        d[3] = fmaf(SCORE_ERROR, v.w, SCORE_TINY);
-    };
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-        if (i % 4 == 0) bounds(i);
-        L = fminf(L, f[i] >= at ? f[i] - d[i % 4] : INFINITY);
-        U = fmaxf(U, f[i] <= vk ? f[i] + d[i % 4] : -INFINITY);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        L = fminf(L, __shfl_xor_sync(0xffffffffu, L, o));
-        U = fmaxf(U, __shfl_xor_sync(0xffffffffu, U, o));
-    }
-    Bits sure = extra, close = 0;
-    if (number && p.qn[row] < INFINITY) {
+        const float d2 = 2.f * fmaf(SCORE_ERROR, key_norm, SCORE_TINY), above = at + d2, below = at - d2;
+        close = 0;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
-            if (i % 4 == 0) bounds(i);
-            const bool in = f[i] - d[i % 4] > U;
-            sure |= (Bits)in << i;
-            close |= (Bits)(!in && f[i] + d[i % 4] >= L) << i;
+            sure |= (Bits)(f[i] > above) << i;
+            close |= (Bits)(f[i] >= below) << i;
         }
-    } else {  // a mean is not finite: all are close
+        close &= allowed & ~sure;
+        if (__reduce_add_sync(0xffffffffu, bits_of(close)) > 32) {
+            float L = INFINITY, U = -INFINITY, vk = INFINITY;
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) close |= (Bits)(f[i] == f[i]) << i;
+            for (int i = 0; i < NPL; ++i) vk = fminf(vk, f[i] >= at ? f[i] : INFINITY);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) vk = fminf(vk, __shfl_xor_sync(0xffffffffu, vk, o));
+            auto bound = [&](int i) { return fmaf(SCORE_ERROR, j0 + i < nk ? __ldg(kn + j0 + i) : 0.f, SCORE_TINY); };
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) {
+                const float d = bound(i);
+                L = fminf(L, f[i] >= at ? f[i] - d : INFINITY);
+                U = fmaxf(U, f[i] <= vk ? f[i] + d : -INFINITY);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                L = fminf(L, __shfl_xor_sync(0xffffffffu, L, o));
+                U = fmaxf(U, __shfl_xor_sync(0xffffffffu, U, o));
+            }
+            sure = extra;
+            close = 0;
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) {
+                const float d = bound(i);
+                sure |= (Bits)(f[i] - d > U) << i;
+                close |= (Bits)(f[i] + d >= L) << i;
+            }
+            close &= allowed & ~sure;
+        }
     }
     const int n_sure = __reduce_add_sync(0xffffffffu, bits_of(sure));
     const int n_close = __reduce_add_sync(0xffffffffu, bits_of(close));
@@ -540,7 +584,7 @@ __global__ void __launch_bounds__(128, NPL <= 24 ? 8 : 1) block_topk_kernel(cons
         return score_key(s);
     };
     if (n_close <= 32) {
-        // lane n ranks the n-th close block among all of them
+        // lane n has the n-th close block
         const int first = before(close);
         Bits rest = close;
         for (int n = first; rest; ++n) {
@@ -549,19 +593,47 @@ __global__ void __launch_bounds__(128, NPL <= 24 ? 8 : 1) block_topk_kernel(cons
             rest ^= low;
         }
         __syncwarp();
-        unsigned long long k = 0;
+        bool in = false, open = lane < n_close;
+        int left = need;
+        if (number) {
+            // their own bounds leave fewer: L and U as above, which no other block decides
+            const int j = again[warp][open ? lane : 0];
+            const float a = reinterpret_cast<const float*>(stage[warp])[j];
+            const float d = fmaf(SCORE_ERROR, __ldg(kn + j), SCORE_TINY);
+            const uint32_t none = 0xffffffffu;
+            const uint32_t vk = __reduce_min_sync(none, open && a >= at ? score_key32(a) : none);
+            const float L = key32_score(__reduce_min_sync(none, open && a >= at ? score_key32(a - d) : none));
+            const float U = key32_score(__reduce_max_sync(none, open && score_key32(a) <= vk ? score_key32(a + d) : 0u));
+            in = open && a - d > U;
+            open = open && !in && a + d >= L;
+            left -= __popc(__ballot_sync(none, in));
+            const unsigned still = __ballot_sync(none, open);
+            if (open) again[warp][__popc(still & ((1u << lane) - 1))] = j;
+            __syncwarp();
+        }
+        // lane n ranks the n-th block that is left among all of them
+        const unsigned still = __ballot_sync(0xffffffffu, open);
+        const int n_open = __popc(still);
+        unsigned chosen = __ballot_sync(0xffffffffu, in);
+        if (n_open == left) {
+            chosen |= still;
+        } else {
+            unsigned long long k = 0;
 #pragma unroll 1
-        for (int c = 0; c < n_close; c += 4) {
-            const unsigned long long e = exact_key(again[warp][min(c + (lane >> 3), n_close - 1)]);
-            const unsigned long long got = __shfl_sync(0xffffffffu, e, (lane & 3) * 8);
-            if (lane >= c && lane < c + 4) k = got;  // c is a multiple of 4: lane & 3 == lane - c
+            for (int c = 0; c < n_open; c += 4) {
+                const unsigned long long e = exact_key(again[warp][min(c + (lane >> 3), n_open - 1)]);
+                const unsigned long long got = __shfl_sync(0xffffffffu, e, (lane & 3) * 8);
+                if (lane >= c && lane < c + 4) k = got;  // c is a multiple of 4: lane & 3 == lane - c
+            }
+            int better = 0;
+            for (int l = 0; l < n_open; ++l) {
+                const unsigned long long other = __shfl_sync(0xffffffffu, k, l);
+                better += other > k || (other == k && l < lane);
+            }
+            const unsigned best = __ballot_sync(0xffffffffu, lane < n_open && better < left);
+            const int mine = __popc(still & ((1u << lane) - 1));  // the lane's own block's place among those left
+            chosen |= __ballot_sync(0xffffffffu, open && (best >> mine & 1));
         }
-        int better = 0;
-        for (int l = 0; l < n_close; ++l) {
-            const unsigned long long other = __shfl_sync(0xffffffffu, k, l);
-            better += other > k || (other == k && l < lane);
-        }
-        const unsigned chosen = __ballot_sync(0xffffffffu, lane < n_close && better < need);
         rest = close;
         for (int n = first; rest; ++n) {
             const Bits low = rest & (~rest + 1);
@@ -767,10 +839,20 @@ cudaError_t launch_block_select(const void* q, long long ldq, const void* k, lon
     }
     const int vecs = heads * 16;
     auto mean = [&](auto kernel, int most, int groups) {
-        const int threads = vecs < most ? (vecs + 31) / 32 * 32 : most;
+        // the column slice that leaves the fewest threads idle, the widest of those (640 vectors:
+        // 160 threads 249 us, 256 with a sixth of them idle 290)
+        int threads = 32, idle = INT_MAX;
+        for (int n = 32; n <= most; n += 32) {
+            const int rest = (vecs + n - 1) / n * n - vecs;
+            if (rest <= idle) {
+                idle = rest;
+                threads = n;
+            }
+        }
         kernel<<<dim3(nq + nk, (vecs + threads - 1) / threads, B), dim3(threads, groups), 0, ctx.stream>>>(
             reinterpret_cast<const __nv_bfloat16*>(q), ldq, reinterpret_cast<const __nv_bfloat16*>(k), ldk, heads, g, oq, ok);
     };
+    // under an SM's 1024 threads on each: four groups of threads per slice
     if ((long long)(nq + nk) * vecs * B < 148 * 1024) mean(block_mean_kernel<4>, 64, 4);
     else mean(block_mean_kernel<1>, 256, 1);
     if (fast) {
