@@ -689,3 +689,41 @@ def test_streams_given_by_handle():
         s.synchronize()
         assert torch.equal(out, want)
     assert torch.cuda.current_stream() != s
+
+
+@pytest.mark.parametrize("nk", [100, 700, 1500])
+def test_block_select_with_keys_of_very_different_length(nk):
+    """Blocks 10^4 times longer than the others, with scores of every size among them: the error bound of the longest
+    would leave the whole row open."""
+    heads, topk = 2, nk // 5
+    args = (heads, (1, 1, 96), (1, 1, nk * 16), (1, 1, 32), (1, 1, 16), topk)
+    q, k = rnd((1, 96, heads * 128), 171), rnd((1, nk * 16, heads * 128), 172)
+    blk = k.view(nk, 16, heads * 128)
+    blk[3::29] = blk[3::29] * 1e4
+    blk[5::31] = blk[5::31] * 30
+    blk[7] = blk[7] * 1e-6
+    mask = (torch.rand((3, nk), generator=torch.Generator().manual_seed(173)) < 0.7).to(torch.uint8)
+    for m in (None, mask):
+        blocks, counts = B().op_block_select(q, k, *args, mask=None if m is None else m.cuda())
+        B().op_sync()
+        want = R.select(q, k, *args, m)
+        assert torch.equal(blocks.cpu(), want[0]) and torch.equal(counts.cpu(), want[1])
+
+
+@pytest.mark.parametrize("nk", [3, 13, 33, 97, 701, 1025])
+@pytest.mark.parametrize("offset", [0, 1, 2, 3])
+def test_block_select_masks_at_any_address(nk, offset):
+    """Mask rows begin at every byte of a word; bytes before and behind the mask must not count."""
+    heads, topk = 1, max(1, nk // 4)
+    args = (heads, (1, 1, 5 * 16), (1, 1, nk * 16), (1, 1, 16), (1, 1, 16), topk)
+    q, k = rnd((1, 80, 128), 181), rnd((1, nk * 16, 128), 182)
+    room = torch.full((5 * nk + 16,), 2, dtype=torch.uint8, device="cuda")
+    mask = room[offset:offset + 5 * nk].view(5, nk)
+    m = torch.randint(0, 8, (5, nk), generator=torch.Generator().manual_seed(183)).to(torch.uint8)
+    m[m < 6] = (m[m < 6] < 3).to(torch.uint8)          # 0 and 1, some of 6 and 7: asked for
+    m[4, :] = 255                                      # any value above 1 asks for a block
+    mask.copy_(m)
+    blocks, counts = B().op_block_select(q, k, *args, mask=mask)
+    B().op_sync()
+    want = R.select(q, k, *args, m.clamp(max=2))
+    assert torch.equal(blocks.cpu(), want[0]) and torch.equal(counts.cpu(), want[1])

@@ -608,6 +608,7 @@ __global__ void __launch_bounds__(128, NPL <= 24 ? 7 : 1) block_topk_kernel(cons
             open = open && !in && a + d >= L;
             left -= __popc(__ballot_sync(none, in));
             const unsigned still = __ballot_sync(none, open);
+            __syncwarp();  // the list has been read
             if (open) again[warp][__popc(still & ((1u << lane) - 1))] = j;
             __syncwarp();
         }
