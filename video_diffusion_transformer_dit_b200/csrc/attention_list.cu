@@ -16,8 +16,8 @@
 // overwritten by its P (bf16, 32 columns).  In step k of its unit a stream issues
 // S(k) = Q K_k^T into the one buffer and O += P(k-1) V_(k-1) from the other, so
 // the softmax finds S(k) finished when it is done with tile k - 1 (with one
-// 128-key S per stream the softmax and the MMAs of a stream took turns: 1.3
-// times the time).  The streams share nothing but the SM: each has its producer,
+// 128-key S per stream the softmax and the MMAs of a stream take turns: 2.0 ms at
+// the 480p size below).  The streams share nothing but the SM: each has its producer,
 // its issuer, its softmax warps and its ring of five 16 KB slots for K and V tiles
 // in the order K(k), V(k - 1).  Stream t walks units blockIdx.x * 2 + t,
 // + 2 * gridDim.x, ...
@@ -28,8 +28,8 @@
 //
 // Warps (registers per thread as in the dense kernel):
 //   0, 2   TMA producer of stream 0 / 1 and the 64-bit mask of each tile's keys (one
-//          producer for both streams was the bottleneck: gathering a tile takes it
-//          about as long as the tile's MMAs);
+//          producer for both streams is the bottleneck: gathering a tile takes it
+//          about as long as the tile's MMAs, 2.6 ms);
 //   1, 3   MMA issuer of stream 0 / 1 (1 owns the tensor memory); it also zeroes the
 //          V rows of a tile past the sequence's end inside a page before its P.V;
 //   4..11  softmax of stream 0 / 1, one query row per thread; warps without a
@@ -40,6 +40,21 @@
 // unit is one range for one head and query tile; it may hold the end of one
 // sequence, whole ones and the beginning of another.  A part of a list writes its
 // normalised fp32 rows and their log-sum-exp, and list_join_kernel joins them.
+//
+// Measured (12 heads, 32760 tokens of a 480p clip; Tflop/s of the tiles computed):
+//   blocks, 336 query blocks of 128 x 78 of 624 key blocks of 64: 1.13-1.2 ms cold, 1.30
+//     in a long run, where the power limit holds the clock at 1.7 GHz; 1.03-1.15 Pflop/s,
+//     tensor pipe 57 %.  A third of the rows and keys are padding of blocks at the grid's
+//     edges.  What bounds it: S = Q K^T with 64 keys reads both operands from shared
+//     memory, 48 clocks where the MMA alone takes 32, and every 128 x 64 tile brings its
+//     own K and V, 10.4 GB, 8 TB/s, over the L2.
+//   pages, one new token on 131040: 122 us, 6.6 TB/s of K and V: memory.
+//   pages, 1560 new tokens on 32760: 363 us with 9 ranges of 156 units, 0.86 Pflop/s.
+// Tried on the 480p blocks and slower: Q in tensor memory and one query tile per CTA with
+// two threads per row (1.4 ms); two warpgroups on alternate tiles of one query tile (1.36
+// in a long run); skipping the MMA steps behind a tile's last key (blocks 1 % faster,
+// pages 2 % slower); P as two bf16 terms for tiles of few rows, which halves the error:
+// one token 15 %, and its registers cost the large tiles 7 %.
 #include <type_traits>
 
 #include "common.cuh"
@@ -842,9 +857,11 @@ cudaError_t init_attention_list_attributes() {
 
 namespace {
 
-// Splits of each list: the number that takes the least time in tile steps.  A
-// unit costs its tiles plus about three steps of filling and draining; a split
-// one also writes its fp32 rows, and the join reads them all again.
+// Splits of each list: the number that takes the least time in tile steps, over the
+// waves of two units per SM.  A unit costs its tiles plus five steps of filling and
+// draining, a split one another for its fp32 rows, and the join reads them all again.
+// In ten shapes (1 to 1560 rows, 30 to 2049 tiles, every number of splits up to 49) its
+// choice was within 3 % of the best one, and 5 % in one; a wave more costs 30 to 50 %.
 int list_splits(long long per, long long max_tiles, int rows) {
     const int streams = 2 * alist::PLAN_SMS;
     if (per <= 0 || per >= 8 * streams) return 1;
