@@ -133,9 +133,9 @@ typedef struct {
 
 /* Key blocks for block-sparse attention.  Per sample and head, query block i
  * scores key block j by the dot product of the mean of its queries and the mean
- * of the block's keys (held in 64 bits: the order of additions does not decide
- * between close scores) and keeps the topk best: equal scores go to the lower
- * block, a NaN ranks with -inf.  mask: uint8 [query blocks, key blocks] shared
+ * of the block's keys (in 64 bits: only scores that agree to the last few of them
+ * can depend on the order of additions) and keeps the topk best: equal scores go to
+ * the lower block, a NaN ranks with -inf.  mask: uint8 [query blocks, key blocks] shared
  * by samples and heads, or NULL; 0 forbids a block, 1 leaves it to its score,
  * any other value takes it ahead of all scores.
  *   blocks  int32 [B, heads, query blocks, topk]: the blocks kept, ascending,

@@ -142,13 +142,18 @@ __global__ void __launch_bounds__(256) block_mean_kernel(const __nv_bfloat16* __
     }
     const MeanOut& o = keys ? ok : oq;
     const long long at = ((long long)b * heads + (mine ? col / 128 : 0)) * (nF * nH * nW) + blk;
-    const double count = (double)n;
+    // a whole block's count is a power of two: the same numbers without eight divisions
+    if ((n & (n - 1)) == 0) {
+        const double part = 1.0 / (double)n;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) acc[c] *= part;
+    } else {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) acc[c] /= (double)n;
+    }
     double ss = 0.0;
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        acc[c] /= count;
-        ss += acc[c] * acc[c];
-    }
+    for (int c = 0; c < 8; ++c) ss += acc[c] * acc[c];
     if (o.unit) {
 #pragma unroll
         for (int x = 8; x > 0; x >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, x);
