@@ -568,15 +568,15 @@ def _elsewhere(device, stream):
     return _th.cuda.stream(stream)
 
 
-def _scratch(nbytes, given, device):
+def _scratch(nbytes, given, like):
     """(pointer, bytes, tensor) of the caller's workspace or of a new one."""
     if given is None:
         if nbytes <= 0:
             return None, 0, None
-        given = _th.empty(nbytes, dtype=_th.uint8, device=device)
+        given = like.new_empty(nbytes, dtype=_th.uint8)
         return given.data_ptr(), nbytes, given
-    if given.device != device or not given.is_contiguous():
-        raise ValueError(f"workspace: a contiguous tensor on {device} is needed, got one on {given.device}")
+    if given.device != like.device or not given.is_contiguous():
+        raise ValueError(f"workspace: a contiguous tensor on {like.device} is needed, got one on {given.device}")
     return given.data_ptr(), given.numel() * given.element_size(), given
 
 
@@ -601,16 +601,16 @@ def op_block_select(q, k, heads, q_grid, k_grid, q_block, k_block, topk, mask=No
     if mask is not None:
         _dense("mask", mask, (p.nq, p.nk), torch.uint8, dev)
     if blocks is None:
-        blocks = torch.empty((B, heads, p.nq, max(topk, 0)), dtype=torch.int32, device=dev)
+        blocks = q.new_empty((B, heads, p.nq, max(topk, 0)), dtype=torch.int32)
     else:
         _dense("blocks", blocks, (B, heads, p.nq, topk), torch.int32, dev)
     if counts is None:
-        counts = torch.empty((B, heads, p.nq), dtype=torch.int32, device=dev)
+        counts = q.new_empty((B, heads, p.nq), dtype=torch.int32)
     else:
         _dense("counts", counts, (B, heads, p.nq), torch.int32, dev)
     if B == 0:
         return blocks, counts
-    ws, nbytes, _keep = _scratch(p.select_bytes, workspace, dev)
+    ws, nbytes, _keep = _scratch(p.select_bytes, workspace, q)
     _check(lib().wan_op_block_select(q.data_ptr(), ldq, k.data_ptr(), ldk, B, heads, p.ref, _ptr(mask), topk,
                                      blocks.data_ptr(), counts.data_ptr(), ws, nbytes, _raw_stream(dev.index)),
            "wan_op_block_select")
@@ -644,7 +644,7 @@ def op_attention_blocks(q, k, v, heads, q_grid, k_grid, q_block, k_block, blocks
         ldo = _rows("out", out, B, p.Lq, D, dev)
     if B == 0:
         return out
-    ws, nbytes, _keep = _scratch(p.attend_bytes, workspace, dev)
+    ws, nbytes, _keep = _scratch(p.attend_bytes, workspace, q)
     _check(lib().wan_op_attention_blocks(q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, out.data_ptr(), ldo, B,
                                          heads, p.ref, blocks.data_ptr(), counts.data_ptr(), topk, _ptr(lse), ws, nbytes,
                                          _raw_stream(dev.index)), "wan_op_attention_blocks")
@@ -736,7 +736,7 @@ def op_attention_paged(q, k_cache, v_cache, table, lens, heads, out=None, lse=No
     if B == 0 or T == 0:
         return out
     need = _paged_bytes(B, heads, T, c.page_stride, c.token_stride, c.num_pages, c.page_size, c.table_ld, c.max_pages)
-    ws, nbytes, _keep = _scratch(need, workspace, dev)
+    ws, nbytes, _keep = _scratch(need, workspace, q)
     _check(lib().wan_op_attention_paged(q.data_ptr(), ldq, C.byref(c), lens.data_ptr(), out.data_ptr(), ldo, B, heads, T,
                                         _ptr(lse), ws, nbytes, _raw_stream(dev.index)), "wan_op_attention_paged")
     return out
