@@ -727,3 +727,54 @@ def test_block_select_masks_at_any_address(nk, offset):
     B().op_sync()
     want = R.select(q, k, *args, m.clamp(max=2))
     assert torch.equal(blocks.cpu(), want[0]) and torch.equal(counts.cpu(), want[1])
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("T", [1, 2, 3])
+def test_attention_paged_of_single_tokens(T, page):
+    """One and two new tokens (a kernel of their own) and three: lengths around the 16 keys of a warp and the 64 of a
+    tile, missing pages, foreign NaN behind the sequences, large logits, strided caches."""
+    heads, per = 5, 1024 // page
+    lens = [0, 1, 15, 16, 17, 63, 64, 65, 127, 129, 500, 1023, 1024, 5000, -3]
+    n = len(lens)
+    room = torch.full((n * per + 2, 2, page, heads * 128 + 8), math.nan, dtype=torch.bfloat16, device="cuda")
+    kc, vc = room[:, 0, :, :heads * 128], room[:, 1, :, :heads * 128]
+    table = torch.randperm(n * per, generator=torch.Generator().manual_seed(191)).view(n, per).to(torch.int32).cuda()
+    for b, length in enumerate(lens):
+        for i in range(per):
+            left = min(max(length, 0), per * page) - i * page
+            if left > 0:
+                p = int(table[b, i])
+                kc[p, :left] = rnd((min(left, page), heads * 128), 1000 * b + i, 4.0)
+                vc[p, :left] = rnd((min(left, page), heads * 128), 1000 * b + i + 500)
+    table[10, ::3] = -1
+    table[11, 1::2] = n * per + 2
+    table[12, :] = -1                                     # nothing is there
+    q = rnd((n, T, 2 * heads * 128), 192, 2.0)[..., :heads * 128]
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    lse = torch.empty((n, heads, T), device="cuda")
+    out = B().op_attention_paged(q, kc, vc, table, ln, heads, lse=lse)
+    B().op_sync()
+    check(out, lse, *R.attention_paged(q, kc, vc, table, ln, heads))
+    assert bool((out[12] == 0).all()) and bool(torch.isneginf(lse[12]).all())
+
+
+@pytest.mark.parametrize("T", [1, 2, 3])
+def test_attention_paged_infinite_logits_follow_the_formula(T):
+    heads, page = 2, 32
+    kc, vc, table = cache(3, 40, page, heads, 201)
+    q = rnd((3, T, heads * 128), 202).abs() + 0.5
+    ln = torch.tensor([1280, 1280, 1280], dtype=torch.int32, device="cuda")
+    kc[int(table[0, 7]), 3, 5] = -math.inf                # head 0: weight 0
+    kc[int(table[1, 9]), 30, 128 + 9] = math.inf          # head 1: inf - inf
+    kc[int(table[2, 1]), 0, 3] = math.nan                 # head 0
+    out = B().op_attention_paged(q, kc, vc, table, ln, heads)
+    B().op_sync()
+    nan = out.isnan().view(3, T, heads, 128)
+    assert not bool(nan[0].any()) and bool(nan[1, :, 1].all()) and not bool(nan[1, :, 0].any())
+    assert bool(nan[2, :, 0].all()) and not bool(nan[2, :, 1].any())
+    kc[int(table[0, 7]), 3, 5] = -3e4                     # as far down as it matters
+    kc[int(table[1, 9]), 30, 128 + 9] = 0
+    kc[int(table[2, 1]), 0, 3] = 0
+    ref = R.attention_paged(q, kc, vc, table, ln, heads)
+    check(out[:1], None, *(x[:1] for x in ref))

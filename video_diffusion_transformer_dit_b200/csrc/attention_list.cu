@@ -4,7 +4,8 @@
 //           attends to the key blocks listed for it (boxes of 16..128 tokens);
 //   pages   the T new tokens of each sequence attend to the sequence's cached
 //           keys and values, which lie in pages of 16..128 tokens.
-// Both are the same loop: a list of token groups, gathered by TMA into tiles of
+// One or two new tokens have a kernel of their own, paged_rows_kernel, on the same ranges
+// of pages.  Otherwise both are the same loop: a list of token groups, gathered by TMA into tiles of
 // 64 keys (a block or page of 128 tokens is two groups), softmax with a running
 // maximum and sum, O += P V per tile.
 //
@@ -48,13 +49,11 @@
 //     edges.  What bounds it: S = Q K^T with 64 keys reads both operands from shared
 //     memory, 48 clocks where the MMA alone takes 32, and every 128 x 64 tile brings its
 //     own K and V, 10.4 GB, 8 TB/s, over the L2.
-//   pages, one new token on 131040: 122 us, 6.6 TB/s of K and V: memory.
 //   pages, 1560 new tokens on 32760: 363 us with 9 ranges of 156 units, 0.86 Pflop/s.
 // Tried on the 480p blocks and slower: Q in tensor memory and one query tile per CTA with
 // two threads per row (1.4 ms); two warpgroups on alternate tiles of one query tile (1.36
 // in a long run); skipping the MMA steps behind a tile's last key (blocks 1 % faster,
-// pages 2 % slower); P as two bf16 terms for tiles of few rows, which halves the error:
-// one token 15 %, and its registers cost the large tiles 7 %.
+// pages 2 % slower).
 #include <type_traits>
 
 #include "common.cuh"
@@ -76,6 +75,7 @@ constexpr int SMASK = SKV + 2 * SLOTS * SLOT_BYTES;
 constexpr int SBAR = SMASK + 2 * MASKS * 8;
 constexpr int SSTART = SBAR + 320;         // pages: first tile of each sequence
 constexpr int MAX_SEQS = 256;              // sequences per launch (pages)
+constexpr int ROWS_MOST = 2;               // new tokens per sequence that paged_rows_kernel takes
 constexpr int SMEM_BYTES = SSTART + (MAX_SEQS + 1) * 4 + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
 constexpr int THREADS = 384;
@@ -135,19 +135,20 @@ __device__ __forceinline__ uint32_t page_ranges(const ListParams& p, uint32_t to
 }
 
 // What one stream works through: next() takes the next list (false: none left).
-// A list without keys comes with n = 0 (blocks also an empty part of a list).
-template <alist::Mode MODE>
+// A list without keys comes with n = 0 (blocks also an empty part of a list).  WIDTH
+// streams per CTA.
+template <alist::Mode MODE, int WIDTH = 2>
 struct ListWalk {
     ListUnit x;
     int u, b;                  // unit; pages: next sequence of the range
     uint32_t lo, hi;           // pages: the unit's range of tiles
     const uint32_t* start;     // pages: first tile of each sequence, [B + 1]
     __device__ __forceinline__ ListWalk(int t, const uint32_t* starts)
-        : u(blockIdx.x * 2 + t - 2 * gridDim.x), b(0x7fffffff), lo(0), hi(0), start(starts) {}
+        : u(blockIdx.x * WIDTH + t - WIDTH * gridDim.x), b(0x7fffffff), lo(0), hi(0), start(starts) {}
 
     __device__ __forceinline__ bool next(const ListParams& p) {
         if constexpr (MODE == alist::BLOCKS) {
-            u += 2 * gridDim.x;
+            u += WIDTH * gridDim.x;
             if (u >= p.units) return false;
             // splits slowest: CTAs that run together read the same tokens of several heads
             const int per = p.nqb * p.heads * p.B;
@@ -178,7 +179,7 @@ struct ListWalk {
                 x.dirty = s1 == end && (x.length & ((1 << p.log_group) - 1)) != 0;
                 return true;
             }
-            u += 2 * gridDim.x;
+            u += WIDTH * gridDim.x;
             if (u >= p.units) return false;
             const int inner = p.nqb * p.heads;
             const uint32_t r = (uint32_t)(u / inner);
@@ -210,6 +211,22 @@ struct ListWalk {
         return true;
     }
 };
+
+// First tile of each sequence (one warp).
+__device__ __forceinline__ void page_starts(const ListParams& p, uint32_t* starts, int lane) {
+    uint32_t before = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        uint32_t n = b0 + lane < p.B ? page_tiles(page_tokens(p, b0 + lane)) : 0u;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t m = __shfl_up_sync(0xffffffffu, n, o);
+            if (lane >= o) n += m;
+        }
+        if (b0 + lane < p.B) starts[b0 + lane + 1] = before + n;
+        before += __shfl_sync(0xffffffffu, n, 31);
+    }
+    if (lane == 0) starts[0] = 0;
+}
 
 // Query token of row r of query tile qt, -1 where the tile has no such row.
 template <alist::Mode MODE>
@@ -298,20 +315,7 @@ __global__ void __launch_bounds__(alist::THREADS, 1)
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
-    if (MODE == PAGES && warp == 2) {
-        uint32_t before = 0;
-        for (int b0 = 0; b0 < p.B; b0 += 32) {
-            uint32_t n = b0 + lane < p.B ? page_tiles(page_tokens(p, b0 + lane)) : 0u;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t m = __shfl_up_sync(0xffffffffu, n, o);
-                if (lane >= o) n += m;
-            }
-            if (b0 + lane < p.B) starts[b0 + lane + 1] = before + n;
-            before += __shfl_sync(0xffffffffu, n, 31);
-        }
-        if (lane == 0) starts[0] = 0;
-    }
+    if (MODE == PAGES && warp == 2) page_starts(p, starts, lane);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -746,6 +750,186 @@ __global__ void __launch_bounds__(alist::THREADS, 1)
     }
 }
 
+// One to R new tokens per sequence: no product is wide enough for the tensor cores, and
+// K and V go through registers once.  A CTA takes one unit (a range of tiles for one
+// head) at a time, its warps 16 keys each in turn: a half warp reads a key's 128 columns
+// (16 bytes per lane, eight keys in flight), and
+//   s_i = sum over 8 columns in fp32 pairs, then over the 16 lanes with the keys
+//         dealt out on the way, so that a lane pair ends with one key's score;
+//   p   = 2^(s - m) per lane pair, m the warp's running maximum;
+//   o  += p_i v_i, p_i fetched from its lanes.
+// p stays fp32.  The warps' (m, l, o) meet in shared memory at the unit's end.
+//
+// Memory bound: one token, 12 heads, 131040 places: 119.8 us cold, 123.2 in a long run (6.6
+// TB/s); a copy of as many bytes takes 123.  The tiles take 127.5 and 133.6, as their MMAs
+// are 128 rows wide all the same: tensor cores and shared memory draw the power that the
+// memory wants, and the clock falls to 1.45 GHz.  4096 places: 10.0 us against 15.1.  Two
+// tokens: 134.8 against 135.5 and 14.1 against 18.5; from three on the arithmetic, 13
+// instructions per key and row beside the 22 that all rows share, bounds it: 224 us
+// against 137.  So R is 1 or 2, two CTAs to an SM (eight keys of K and V in flight per
+// lane, 116 and 128 registers).
+template <int R>
+__global__ void __launch_bounds__(256, 2) paged_rows_kernel(const __nv_bfloat16* __restrict__ q, long long ldq,
+                                                            const __nv_bfloat16* __restrict__ k,
+                                                            const __nv_bfloat16* __restrict__ v,
+                                                            long long page_stride, long long token_stride,
+                                                            const __grid_constant__ ListParams p) {
+    using namespace alist;
+    __shared__ uint32_t starts[MAX_SEQS + 1];
+    __shared__ float warp_m[8][R], warp_l[8][R];
+    __shared__ __align__(16) float warp_o[8][R][128];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == 0) page_starts(p, starts, lane);
+    __syncthreads();
+    if (p.splits > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int sub = lane >> 4, col = (lane & 15) * 8;
+    const int log_page = p.log_group + p.log_sub;
+    auto pairs = [](const uint4& x, uint64_t (&y)[4]) {
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) y[c] = f2pack(__uint_as_float(w[c] << 16), __uint_as_float(w[c] & 0xffff0000u));
+    };
+    auto fetch = [](const __nv_bfloat16* at) {
+        uint4 x;
+        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                     : "l"(at));
+        return x;
+    };
+    ListWalk<PAGES, 1> w(0, starts);
+    while (w.next(p)) {
+        const ListUnit x = w.x;
+        uint64_t q2[R][4], acc[R][4];
+        float m[R], l[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const uint4 row = r < p.T ? __ldg(reinterpret_cast<const uint4*>(q + ((long long)x.b * p.T + r) * ldq + x.h * 128 + col))
+                                      : make_uint4(0, 0, 0, 0);
+            pairs(row, q2[r]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                q2[r][c] = mul2(q2[r][c], f2pack(p.scale_log2, p.scale_log2));
+                acc[r][c] = 0ull;
+            }
+            m[r] = -INFINITY;
+            l[r] = 0.f;
+        }
+        const int end = x.n > 0 ? min(x.length, (x.j0 + x.n) * KEYS) : 0;
+        const int* table = p.table + (long long)x.b * p.table_ld;
+        int k0 = x.j0 * KEYS + warp * 16;
+        int page = k0 < end ? __ldg(table + (k0 >> log_page)) : -1;
+        for (; k0 < end; k0 += 128) {
+            const int here = page;
+            page = k0 + 128 < end ? __ldg(table + ((k0 + 128) >> log_page)) : -1;
+            if (here < 0 || here >= p.num_pages) continue;
+            const long long at = here * page_stride + ((k0 & ((1 << log_page) - 1)) + sub) * token_stride + x.h * 128 + col;
+            const int left = end - k0 - sub;  // keys 0, 2, 4 ... of this half warp
+            uint4 kx[8], vx[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) kx[i] = 2 * i < left ? fetch(k + at + 2 * i * token_stride) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) vx[i] = 2 * i < left ? fetch(v + at + 2 * i * token_stride) : make_uint4(0, 0, 0, 0);
+            float s[R][8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                uint64_t y[4];
+                pairs(kx[i], y);
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    uint64_t d = mul2(y[0], q2[r][0]);
+#pragma unroll
+                    for (int c = 1; c < 4; ++c) d = fma2(y[c], q2[r][c], d);
+                    float a, b;
+                    f2unpack(d, a, b);
+                    s[r][i] = a + b;
+                }
+            }
+            float prob[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                // over the half warp, half of the keys handed over per step
+#pragma unroll
+                for (int o = 8, n = 4; o >= 2; o >>= 1, n >>= 1) {
+#pragma unroll
+                    for (int i = 0; i < n; ++i) {
+                        const float keep = lane & o ? s[r][n + i] : s[r][i], give = lane & o ? s[r][i] : s[r][n + i];
+                        s[r][i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                    }
+                }
+                float t = s[r][0] + __shfl_xor_sync(0xffffffffu, s[r][0], 1);
+                const int mine = (lane >> 3 & 1) * 4 + (lane >> 2 & 1) * 2 + (lane >> 1 & 1);
+                if (2 * mine >= left) t = -INFINITY;
+                float top = t;
+#pragma unroll
+                for (int o = 16; o >= 2; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                if (top > m[r]) {  // the whole warp alike
+                    const float a = ex2_approx(m[r] - top);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) acc[r][c] = mul2(acc[r][c], f2pack(a, a));
+                    l[r] *= a;
+                    m[r] = top;
+                }
+                prob[r] = ex2_approx(t - (m[r] == -INFINITY ? 0.f : m[r]));
+                l[r] += prob[r];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                uint64_t y[4];
+                pairs(vx[i], y);
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float pi = __shfl_sync(0xffffffffu, prob[r], (lane & 16) | (i >> 2 & 1) * 8 | (i >> 1 & 1) * 4 | (i & 1) * 2);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) acc[r][c] = fma2(y[c], f2pack(pi, pi), acc[r][c]);
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
+            float y[8];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) f2unpack(acc[r][c], y[2 * c], y[2 * c + 1]);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) y[c] += __shfl_xor_sync(0xffffffffu, y[c], 16);
+            if (lane < 16) {
+                *reinterpret_cast<float4*>(&warp_o[warp][r][col]) = make_float4(y[0], y[1], y[2], y[3]);
+                *reinterpret_cast<float4*>(&warp_o[warp][r][col + 4]) = make_float4(y[4], y[5], y[6], y[7]);
+            }
+            if (lane == 0) {
+                warp_m[warp][r] = m[r];
+                warp_l[warp][r] = 0.5f * l[r];  // two lanes had each key
+            }
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < p.T * 128; e += 256) {
+            const int r = e >> 7, d = e & 127;
+            float top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, warp_m[i][r]);
+            float total = 0.f, o = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float f = warp_m[i][r] == -INFINITY ? 0.f : ex2_approx(warp_m[i][r] - top);
+                total += f * warp_l[i][r];
+                o += f * warp_o[i][r][d];
+            }
+            const bool none = total == 0.f;
+            o *= none ? 0.f : 1.0f / total;
+            const float lse2 = none ? -INFINITY : top + log2f(total);
+            if (x.part >= 0) {
+                p.part_o[(x.part * p.rows + r) * 128 + d] = o;
+                if (d == 0) p.part_lse[x.part * p.rows + r] = lse2;
+            } else {
+                p.o[((long long)x.b * p.T + r) * p.ldo + x.h * 128 + d] = __float2bfloat16(o);
+                if (d == 0 && p.lse) p.lse[((long long)x.b * p.heads + x.h) * p.T + r] = lse2 * 0.6931471805599453f;
+            }
+        }
+        __syncthreads();
+    }
+}
+
 // Joins the parts of one query row's list: O = sum_s w_s O_s, w_s = 2^(lse_s -
 // lse); a part without keys has lse -inf and is not read.  A CTA takes JOIN_ROWS
 // rows of one query tile, two per warp: it is latency that bounds it (the first
@@ -882,9 +1066,9 @@ int list_splits(long long per, long long max_tiles, int rows) {
 
 long long list_workspace(long long parts, int rows) { return parts * rows * 129ll * 4; }
 
-template <alist::Mode MODE>
-cudaError_t launch_list(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, ListParams& p, void* ws,
-                        const LaunchCtx& ctx) {
+// The kernel over p's units, launch(), and the join of split lists.
+template <alist::Mode MODE, typename Launch>
+cudaError_t launch_list(ListParams& p, void* ws, const LaunchCtx& ctx, Launch launch) {
     const long long per = (long long)p.nqb * p.heads * p.B;
     p.units = MODE == alist::BLOCKS ? (int)(per * p.splits) : p.nqb * p.heads * p.splits;
     if (p.splits > 1) {
@@ -894,8 +1078,7 @@ cudaError_t launch_list(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
     p.scale_log2 = 1.4426950408889634f / sqrtf(128.0f);
     p.wc.err = ctx.err;
     p.wc.limit_ns = ctx.wait_limit_ns;
-    const int ctas = (p.units + 1) / 2;
-    attn_list_kernel<MODE><<<ctas < ctx.num_sms ? ctas : ctx.num_sms, alist::THREADS, alist::SMEM_BYTES, ctx.stream>>>(tq, tk, tv, p);
+    launch();
     if (ctx.launches) ++*ctx.launches;
     if (p.splits > 1) {
         cudaLaunchConfig_t cfg{};
@@ -912,6 +1095,26 @@ cudaError_t launch_list(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
         if (ctx.launches) ++*ctx.launches;
     }
     return cudaGetLastError();
+}
+
+template <alist::Mode MODE>
+cudaError_t launch_tiles(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, ListParams& p, void* ws,
+                         const LaunchCtx& ctx) {
+    return launch_list<MODE>(p, ws, ctx, [&] {
+        const int ctas = (p.units + 1) / 2;
+        attn_list_kernel<MODE><<<ctas < ctx.num_sms ? ctas : ctx.num_sms, alist::THREADS, alist::SMEM_BYTES, ctx.stream>>>(
+            tq, tk, tv, p);
+    });
+}
+
+template <int R>
+cudaError_t launch_rows(const void* q, long long ldq, const KvPages& c, ListParams& p, void* ws, const LaunchCtx& ctx) {
+    return launch_list<alist::PAGES>(p, ws, ctx, [&] {
+        const int most = 2 * ctx.num_sms;  // resident
+        paged_rows_kernel<R><<<p.units < most ? p.units : most, 256, 0, ctx.stream>>>(
+            reinterpret_cast<const __nv_bfloat16*>(q), ldq, reinterpret_cast<const __nv_bfloat16*>(c.k),
+            reinterpret_cast<const __nv_bfloat16*>(c.v), c.page_stride, c.token_stride, p);
+    });
 }
 
 int log2_of(int v) {
@@ -1011,7 +1214,7 @@ cudaError_t launch_attention_blocks(const void* q, long long ldq, const void* k,
     CUtensorMap tq, tk, tv;
     if (!map(&tq, q, ldq, g.q, g.qb) || !map(&tk, k, ldk, g.k, p.sub) || !map(&tv, v, ldv, g.k, p.sub))
         return cudaErrorInvalidValue;
-    return launch_list<alist::BLOCKS>(tq, tk, tv, p, ws, ctx);
+    return launch_tiles<alist::BLOCKS>(tq, tk, tv, p, ws, ctx);
 }
 
 cudaError_t launch_attention_paged(const void* q, long long ldq, const KvPages& c, const int* lens, void* o,
@@ -1028,14 +1231,19 @@ cudaError_t launch_attention_paged(const void* q, long long ldq, const KvPages& 
         p.o = reinterpret_cast<__nv_bfloat16*>(o) + (long long)b0 * T * ldo;
         p.ldo = ldo;
         p.lse = lse ? lse + (long long)b0 * heads * T : nullptr;
-        const uint32_t group = 1u << p.log_group;
         const void* q0 = reinterpret_cast<const __nv_bfloat16*>(q) + (long long)b0 * T * ldq;
-        CUtensorMap tq, tk, tv;
-        if (!make_tmap_3d(&tq, q0, width, T, n, ldq, (uint64_t)ldq * T, 64, 128) ||
-            !make_tmap_3d(&tk, c.k, width, c.page_size, c.num_pages, c.token_stride, c.page_stride, 64, group) ||
-            !make_tmap_3d(&tv, c.v, width, c.page_size, c.num_pages, c.token_stride, c.page_stride, 64, group))
-            return cudaErrorInvalidValue;
-        const cudaError_t e = launch_list<alist::PAGES>(tq, tk, tv, p, ws, ctx);
+        cudaError_t e;
+        if (T <= alist::ROWS_MOST) {
+            e = T == 1 ? launch_rows<1>(q0, ldq, c, p, ws, ctx) : launch_rows<2>(q0, ldq, c, p, ws, ctx);
+        } else {
+            const uint32_t group = 1u << p.log_group;
+            CUtensorMap tq, tk, tv;
+            if (!make_tmap_3d(&tq, q0, width, T, n, ldq, (uint64_t)ldq * T, 64, 128) ||
+                !make_tmap_3d(&tk, c.k, width, c.page_size, c.num_pages, c.token_stride, c.page_stride, 64, group) ||
+                !make_tmap_3d(&tv, c.v, width, c.page_size, c.num_pages, c.token_stride, c.page_stride, 64, group))
+                return cudaErrorInvalidValue;
+            e = launch_tiles<alist::PAGES>(tq, tk, tv, p, ws, ctx);
+        }
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
