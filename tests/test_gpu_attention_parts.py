@@ -778,3 +778,16 @@ def test_attention_paged_infinite_logits_follow_the_formula(T):
     kc[int(table[2, 1]), 0, 3] = 0
     ref = R.attention_paged(q, kc, vc, table, ln, heads)
     check(out[:1], None, *(x[:1] for x in ref))
+
+
+@pytest.mark.parametrize("T", [1, 2])
+def test_attention_paged_of_many_sequences(T):
+    """More lists than units that fill the GPU, of all lengths from none to three pages."""
+    n, heads, page = 270, 3, 32
+    kc, vc, table = cache(n, 3, page, heads, 211)
+    q = rnd((n, T, heads * 128), 212)
+    ln = (torch.arange(n, dtype=torch.int32) * 7 % 97).cuda()
+    lse = torch.empty((n, heads, T), device="cuda")
+    out = B().op_attention_paged(q, kc, vc, table, ln, heads, lse=lse)
+    B().op_sync()
+    check(out, lse, *R.attention_paged(q, kc, vc, table, ln, heads))

@@ -106,6 +106,7 @@ struct ListParams {
     long long table_ld;
     const int* lens;
     int max_pages, num_pages, T;
+    int row_warps;          // warps per CTA of paged_rows_kernel
     __nv_bfloat16* o;
     long long ldo;
     float* lse;             // [B, heads, query tokens] or null
@@ -766,22 +767,25 @@ __global__ void __launch_bounds__(alist::THREADS, 1)
 // memory wants, and the clock falls to 1.45 GHz.  4096 places: 10.0 us against 15.1.  Two
 // tokens: 134.8 against 135.5 and 14.1 against 18.5; from three on the arithmetic, 13
 // instructions per key and row beside the 22 that all rows share, bounds it: 224 us
-// against 137.  So R is 1 or 2, two CTAs to an SM (eight keys of K and V in flight per
-// lane, 116 and 128 registers).
-template <int R>
-__global__ void __launch_bounds__(256, 2) paged_rows_kernel(const __nv_bfloat16* __restrict__ q, long long ldq,
+// against 137.  So R is 1 or 2; 16 warps to an SM (eight keys of K and V in flight per
+// lane, 116 and 128 registers), in two CTAs, or in four where there are more lists than
+// such units: each list ends with the meeting of its warps (256 sequences of 64 tokens: 34.5
+// against 44.1 us, of 130: 52 against 64; one of 4096: 11.9 against 10.1, more parts to join).
+template <int R, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) paged_rows_kernel(const __nv_bfloat16* __restrict__ q, long long ldq,
                                                             const __nv_bfloat16* __restrict__ k,
                                                             const __nv_bfloat16* __restrict__ v,
                                                             long long page_stride, long long token_stride,
                                                             const __grid_constant__ ListParams p) {
     using namespace alist;
     __shared__ uint32_t starts[MAX_SEQS + 1];
-    __shared__ float warp_m[8][R], warp_l[8][R];
-    __shared__ __align__(16) float warp_o[8][R][128];
+    __shared__ float warp_m[WARPS][R], warp_l[WARPS][R];
+    __shared__ __align__(16) float warp_o[WARPS][R][128];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == 0) page_starts(p, starts, lane);
     __syncthreads();
     if (p.splits > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    constexpr int STEP = WARPS * 16;
     const int sub = lane >> 4, col = (lane & 15) * 8;
     const int log_page = p.log_group + p.log_sub;
     auto pairs = [](const uint4& x, uint64_t (&y)[4]) {
@@ -818,9 +822,9 @@ __global__ void __launch_bounds__(256, 2) paged_rows_kernel(const __nv_bfloat16*
         const int* table = p.table + (long long)x.b * p.table_ld;
         int k0 = x.j0 * KEYS + warp * 16;
         int page = k0 < end ? __ldg(table + (k0 >> log_page)) : -1;
-        for (; k0 < end; k0 += 128) {
+        for (; k0 < end; k0 += STEP) {
             const int here = page;
-            page = k0 + 128 < end ? __ldg(table + ((k0 + 128) >> log_page)) : -1;
+            page = k0 + STEP < end ? __ldg(table + ((k0 + STEP) >> log_page)) : -1;
             if (here < 0 || here >= p.num_pages) continue;
             const long long at = here * page_stride + ((k0 & ((1 << log_page) - 1)) + sub) * token_stride + x.h * 128 + col;
             const int left = end - k0 - sub;  // keys 0, 2, 4 ... of this half warp
@@ -903,14 +907,14 @@ __global__ void __launch_bounds__(256, 2) paged_rows_kernel(const __nv_bfloat16*
             }
         }
         __syncthreads();
-        for (int e = threadIdx.x; e < p.T * 128; e += 256) {
+        for (int e = threadIdx.x; e < p.T * 128; e += WARPS * 32) {
             const int r = e >> 7, d = e & 127;
             float top = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) top = fmaxf(top, warp_m[i][r]);
+            for (int i = 0; i < WARPS; ++i) top = fmaxf(top, warp_m[i][r]);
             float total = 0.f, o = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < WARPS; ++i) {
                 const float f = warp_m[i][r] == -INFINITY ? 0.f : ex2_approx(warp_m[i][r] - top);
                 total += f * warp_l[i][r];
                 o += f * warp_o[i][r][d];
@@ -1046,8 +1050,7 @@ namespace {
 // draining, a split one another for its fp32 rows, and the join reads them all again.
 // In ten shapes (1 to 1560 rows, 30 to 2049 tiles, every number of splits up to 49) its
 // choice was within 3 % of the best one, and 5 % in one; a wave more costs 30 to 50 %.
-int list_splits(long long per, long long max_tiles, int rows) {
-    const int streams = 2 * alist::PLAN_SMS;
+int list_splits(long long per, long long max_tiles, int rows, int streams = 2 * alist::PLAN_SMS) {
     if (per <= 0 || per >= 8 * streams) return 1;
     int best = 1;
     double least = 1e30;
@@ -1107,11 +1110,11 @@ cudaError_t launch_tiles(const CUtensorMap& tq, const CUtensorMap& tk, const CUt
     });
 }
 
-template <int R>
+template <int R, int WARPS>
 cudaError_t launch_rows(const void* q, long long ldq, const KvPages& c, ListParams& p, void* ws, const LaunchCtx& ctx) {
     return launch_list<alist::PAGES>(p, ws, ctx, [&] {
-        const int most = 2 * ctx.num_sms;  // resident
-        paged_rows_kernel<R><<<p.units < most ? p.units : most, 256, 0, ctx.stream>>>(
+        const int most = 16 / WARPS * ctx.num_sms;  // resident
+        paged_rows_kernel<R, WARPS><<<p.units < most ? p.units : most, WARPS * 32, 0, ctx.stream>>>(
             reinterpret_cast<const __nv_bfloat16*>(q), ldq, reinterpret_cast<const __nv_bfloat16*>(c.k),
             reinterpret_cast<const __nv_bfloat16*>(c.v), c.page_stride, c.token_stride, p);
     });
@@ -1168,7 +1171,9 @@ bool pages_plan(int B, int heads, int T, int max_pages, int page_size, ListParam
     list_groups(page_size, p);
     const long long inner = (long long)p->nqb * heads;
     const long long tiles = ((long long)max_pages << (p->log_sub + p->log_group)) / alist::KEYS + 1;
-    p->splits = list_splits(inner, tiles * B, p->rows);
+    p->row_warps = inner * B > 2 * alist::PLAN_SMS ? 4 : 8;
+    p->splits = list_splits(inner, tiles * B, p->rows,
+                            T > alist::ROWS_MOST ? 2 * alist::PLAN_SMS : 16 / p->row_warps * alist::PLAN_SMS);
     return inner * p->splits < (1ll << 30);
 }
 
@@ -1234,7 +1239,8 @@ cudaError_t launch_attention_paged(const void* q, long long ldq, const KvPages& 
         const void* q0 = reinterpret_cast<const __nv_bfloat16*>(q) + (long long)b0 * T * ldq;
         cudaError_t e;
         if (T <= alist::ROWS_MOST) {
-            e = T == 1 ? launch_rows<1>(q0, ldq, c, p, ws, ctx) : launch_rows<2>(q0, ldq, c, p, ws, ctx);
+            e = T == 1 ? (p.row_warps == 4 ? launch_rows<1, 4>(q0, ldq, c, p, ws, ctx) : launch_rows<1, 8>(q0, ldq, c, p, ws, ctx))
+                       : (p.row_warps == 4 ? launch_rows<2, 4>(q0, ldq, c, p, ws, ctx) : launch_rows<2, 8>(q0, ldq, c, p, ws, ctx));
         } else {
             const uint32_t group = 1u << p.log_group;
             CUtensorMap tq, tk, tv;
