@@ -148,9 +148,9 @@ typedef struct {
  * streams, and graphs that may be replayed at the same time, need their own.
  * Errors before any launch: WAN_EINVAL for a null pointer, WAN_ESHAPE for sizes
  * outside the limits above, topk outside [1, key blocks], more than 28800 key
- * blocks, B * heads > 65535, a leading dimension below 128 * heads or not a
- * multiple of 8, pointers of q, k or workspace that are not 16-byte aligned or
- * a workspace that is too small.  B = 0 launches nothing.                    */
+ * blocks or 2097120 query blocks, B * heads > 65535, a leading dimension below
+ * 128 * heads or not a multiple of 8, pointers of q, k or workspace that are not
+ * 16-byte aligned or a workspace that is too small.  B = 0 launches nothing.  */
 WANDIT_API wan_status wan_op_block_select(const void* q, int64_t ldq, const void* k, int64_t ldk, int B, int heads,
                                           const wan_block_grid* g, const uint8_t* mask, int topk, int32_t* blocks,
                                           int32_t* counts, void* workspace, int64_t workspace_bytes, void* stream);

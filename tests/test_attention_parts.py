@@ -185,3 +185,20 @@ def test_append_refuses_more_rows_than_its_grid_holds(lib):
     for B, T in ((1, (1 << 29) + 1), (1 << 15, 1 << 15)):
         assert lib.wan_op_kv_append(FAKE, 256, FAKE, 256, B, T, 2, FAKE, None, None, 1e-6, 0, 0, 0, 0, 0, 0, 1e4, None, 0, None,
                                     None, 0, 0, C.byref(c), None) == ESHAPE
+
+
+@pytest.mark.parametrize("B,heads", [(1, 1), (1, 32), (2, 40)])
+@pytest.mark.parametrize("g", [dict(q=(1, 1, 64), k=(1, 1, 16 * 28801), qb=(1, 1, 64), kb=(1, 1, 16)),      # key blocks
+                               dict(q=(1, 1, 65535 * 32 + 1), k=(1, 1, 64), qb=(1, 1, 1), kb=(1, 1, 16)),   # query blocks
+                               # with 32 heads the bytes of its scores are 2^64 and more
+                               dict(q=(1, 1, 1 << 30), k=(1, 1, 1 << 30), qb=(1, 1, 1), kb=(1, 1, 16))])
+def test_block_select_names_no_workspace_for_grids_it_refuses(lib, g, B, heads):
+    g = grid(**g)
+    assert lib.wan_op_block_select_workspace(B, heads, C.byref(g)) == -1
+    assert lib.wan_op_block_select(FAKE, 128 * heads, FAKE, 128 * heads, B, heads, C.byref(g), None, 1, FAKE, FAKE, FAKE, BIG,
+                                   None) == ESHAPE
+
+
+def test_block_select_names_a_workspace_for_the_largest_grid_it_takes(lib):
+    g = grid(q=(1, 1, 65535 * 32), k=(1, 1, 16 * 28800), qb=(1, 1, 1), kb=(1, 1, 16))
+    assert lib.wan_op_block_select_workspace(1, 512, C.byref(g)) > 65535 * 32 * 28800 * 512 * 8

@@ -1419,6 +1419,7 @@ bool aligned16(std::initializer_list<const void*> ptrs) {
 bool ld_ok(int64_t ld, int heads) { return ld >= 128ll * heads && ld % 8 == 0 && ld < (1ll << 31); }
 
 constexpr int MAX_LIST = 1 << 24;  // entries of a list of key blocks (times two groups each, still an int)
+constexpr int MAX_SELECT_ROWS = 65535 * 32;  // query blocks per sample and head of a selection (its grids' second axis)
 
 bool group_ok(int64_t n) { return n == 16 || n == 32 || n == 64 || n == 128; }
 
@@ -1437,6 +1438,12 @@ bool block_grid_ok(const wan_block_grid* g, int B, int heads, wan::BlockGrid* ou
     return group_ok(vk) && (int64_t)std::max(B, 1) * std::max(lq, lk) <= (1ll << 31);
 }
 
+// A grid whose rows of scores block selection takes (its workspace fits 64 bits then: below 2^56 bytes).
+bool select_grid_ok(const wan_block_grid* g, int B, int heads, wan::BlockGrid* out) {
+    return block_grid_ok(g, B, heads, out) && out->k_blocks() <= wan::block_select_max_blocks() &&
+           out->q_blocks() <= MAX_SELECT_ROWS;
+}
+
 bool kv_cache_ok(const wan_kv_cache* c, int heads, wan::KvPages* out) {
     *out = wan::KvPages{c->k, c->v, c->page_stride, c->token_stride, c->num_pages, c->page_size, c->table, c->table_ld, c->max_pages};
     if (!group_ok(c->page_size) || c->num_pages < 1 || c->max_pages < 1 || c->table_ld < c->max_pages) return false;
@@ -1449,7 +1456,7 @@ bool kv_cache_ok(const wan_kv_cache* c, int heads, wan::KvPages* out) {
 
 int64_t wan_op_block_select_workspace(int B, int heads, const wan_block_grid* g) {
     wan::BlockGrid bg;
-    if (!g || !block_grid_ok(g, B, heads, &bg)) return -1;
+    if (!g || !select_grid_ok(g, B, heads, &bg)) return -1;
     return wan::block_select_workspace(B, heads, bg);
 }
 
@@ -1458,10 +1465,9 @@ wan_status wan_op_block_select(const void* q, int64_t ldq, const void* k, int64_
                                void* workspace, int64_t workspace_bytes, void* stream) {
     if (!q || !k || !g || !blocks || !counts || !workspace) return WAN_EINVAL;
     wan::BlockGrid bg;
-    if (!block_grid_ok(g, B, heads, &bg) || !ld_ok(ldq, heads) || !ld_ok(ldk, heads) || !aligned16({q, k, workspace}))
+    if (!select_grid_ok(g, B, heads, &bg) || !ld_ok(ldq, heads) || !ld_ok(ldk, heads) || !aligned16({q, k, workspace}))
         return WAN_ESHAPE;
-    const int nk = bg.k_blocks(), nq = bg.q_blocks();
-    if (topk < 1 || topk > nk || nk > wan::block_select_max_blocks() || nq > 65535 * 32) return WAN_ESHAPE;
+    if (topk < 1 || topk > bg.k_blocks()) return WAN_ESHAPE;
     if (workspace_bytes < wan::block_select_workspace(B, heads, bg)) return WAN_ESHAPE;
     if (B == 0) return WAN_OK;
     LaunchCtx ctx;
