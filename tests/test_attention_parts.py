@@ -202,3 +202,19 @@ def test_block_select_names_no_workspace_for_grids_it_refuses(lib, g, B, heads):
 def test_block_select_names_a_workspace_for_the_largest_grid_it_takes(lib):
     g = grid(q=(1, 1, 65535 * 32), k=(1, 1, 16 * 28800), qb=(1, 1, 1), kb=(1, 1, 16))
     assert lib.wan_op_block_select_workspace(1, 512, C.byref(g)) > 65535 * 32 * 28800 * 512 * 8
+
+
+def test_python_selection_refuses_sizes_by_their_own_status(lib, monkeypatch):
+    """A box, a grid or a topk outside the limits is WAN_ESHAPE, not the null workspace that the wrapper has for it,
+    and nothing is allocated for it."""
+    import torch
+    from video_diffusion_transformer_dit_b200 import binding
+    monkeypatch.setattr(binding, "_elsewhere", lambda device, stream: None)      # host tensors: refused all the same
+    x = torch.zeros(1, 192, 12 * 128, dtype=torch.bfloat16)
+    room = torch.zeros(1 << 20, dtype=torch.uint8)
+    for kb, topk in (((1, 3, 5), 3), ((1, 4, 4), 0), ((1, 4, 4), -1), ((1, 4, 4), 13), ((1, 4, 4), (1 << 31) - 1),
+                     ((1, 4, 4), (1 << 32) + 3)):
+        for workspace in (None, room):
+            with pytest.raises(binding.WanError) as e:
+                binding.op_block_select(x, x, 12, (3, 8, 8), (3, 8, 8), (1, 8, 8), kb, topk, workspace=workspace)
+            assert e.value.name == "WAN_ESHAPE", (kb, topk)

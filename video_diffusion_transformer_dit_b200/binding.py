@@ -19,6 +19,7 @@ LIB_PATH = os.path.join(_HERE, "libwandit.so")
 WAN_STATUS = {0: "WAN_OK", 1: "WAN_EINVAL", 2: "WAN_ESHAPE", 3: "WAN_ENOMEM", 4: "WAN_ENOWEIGHTS",
               5: "WAN_EMISSING_WEIGHT", 6: "WAN_EUNEXPECTED_WEIGHT", 7: "WAN_ECUDA", 8: "WAN_ETIMEOUT",
               9: "WAN_EINTERNAL", 10: "WAN_EUNSUPPORTED"}
+WAN_ESHAPE = 2
 WAN_DTYPE_F32, WAN_DTYPE_BF16 = 0, 1
 WAN_OPT_GRAPH, WAN_OPT_WAIT_LIMIT_NS, WAN_OPT_KERNEL_TIMING, WAN_OPT_GEMM_PAIR = 1, 2, 3, 4
 KERNEL_CLASSES = {"patchify": 0, "gemm": 1, "self_attention": 2, "cross_attention": 3, "layernorm": 4,
@@ -569,7 +570,8 @@ def _elsewhere(device, stream):
 
 
 def _scratch(nbytes, given, like):
-    """(pointer, bytes, tensor) of the caller's workspace or of a new one."""
+    """(pointer, bytes, tensor) of the caller's workspace or of a new one; nbytes < 0: none is named, the call
+    refuses its sizes."""
     if given is None:
         if nbytes <= 0:
             return None, 0, None
@@ -597,11 +599,13 @@ def op_block_select(q, k, heads, q_grid, k_grid, q_block, k_block, topk, mask=No
             return op_block_select(q, k, heads, q_grid, k_grid, q_block, k_block, topk, mask, blocks, counts, workspace)
     B = q.shape[0]
     p = _block_plan(B, heads, tuple(q_grid), tuple(k_grid), tuple(q_block), tuple(k_block), topk)
+    if p.select_bytes < 0 or not 1 <= topk <= p.nk:     # as the call would, before its buffers are allocated
+        raise WanError(WAN_ESHAPE, "wan_op_block_select")
     ldq, ldk = _rows("q", q, B, p.Lq, heads * 128, dev), _rows("k", k, B, p.Lk, heads * 128, dev)
     if mask is not None:
         _dense("mask", mask, (p.nq, p.nk), torch.uint8, dev)
     if blocks is None:
-        blocks = q.new_empty((B, heads, p.nq, max(topk, 0)), dtype=torch.int32)
+        blocks = q.new_empty((B, heads, p.nq, topk), dtype=torch.int32)
     else:
         _dense("blocks", blocks, (B, heads, p.nq, topk), torch.int32, dev)
     if counts is None:
