@@ -399,6 +399,9 @@ __global__ void __launch_bounds__(alist::THREADS, 1)
                     w[c] = __ballot_sync(0xffffffffu, in);
                 }
                 if (lane == 0) *dst = make_uint2(w[0], w[1]);
+                // before the elected lane's arrival on the tile's barrier, which publishes the mask:
+                // votes and shuffles between the two order no memory
+                __syncwarp();
             };
             // the tile's groups into a slot: coordinates broadcast, one lane issues all copies from
             // uniform registers (a copy per lane is issued lane by lane, three times as slow)
