@@ -145,3 +145,31 @@ def rotated(x, slot, heads, hw, gain, eps=1e-6, split=(44, 42, 42), theta=10000.
                            for a, w in enumerate(split)], -1)
         x = torch.view_as_real(torch.view_as_complex(x.contiguous()) * torch.polar(torch.ones_like(angle), angle)[:, None])
     return x.reshape(-1, heads * HD), size
+
+
+def block_means(x, heads, grid, block):
+    """Mean of each block [B, heads, blocks, 128] in 64 bits, its tokens added one after the other in token order."""
+    of, n = block_of(grid, block, x.device), block_count(grid, block)
+    order = of.argsort(stable=True)
+    count = torch.bincount(of, minlength=n)
+    place = torch.arange(of.numel(), device=x.device) - (count.cumsum(0) - count)[of[order]]
+    token = torch.full((n, volume(block)), of.numel(), device=x.device)
+    token[of[order], place] = order
+    x = torch.cat((x, torch.zeros_like(x[:, :1])), 1)
+    total = torch.zeros(x.shape[0], n, x.shape[2], dtype=DT, device=x.device)
+    for t in range(volume(block)):
+        total += torch.where((token[:, t] < of.numel())[:, None], x[:, token[:, t]].to(DT), 0.0)
+    return (total / count.to(DT)[:, None]).view(x.shape[0], n, heads, HD).transpose(1, 2)
+
+
+def select_rows(q, k, heads, qg, kg, qb, kb, topk, mask=None):
+    """What select() gives, by sorting all rows at once on the tensors' device."""
+    score = block_means(q, heads, qg, qb) @ block_means(k, heads, kg, kb).transpose(-1, -2)
+    nk = score.shape[-1]
+    kind = torch.ones(score.shape[-2:], dtype=torch.long) if mask is None else mask.cpu().clamp(max=2).long()
+    kind = kind.to(score.device).expand(score.shape)
+    score = torch.where(kind == 2, 0.0, torch.where(score.isnan(), -math.inf, score))
+    rank = score.argsort(dim=-1, descending=True, stable=True)
+    rank = rank.gather(-1, kind.gather(-1, rank).argsort(dim=-1, descending=True, stable=True))[..., :topk]
+    keep = torch.where(kind.gather(-1, rank) > 0, rank, nk).sort(-1).values
+    return torch.where(keep < nk, keep, -1).int().cpu(), (keep < nk).sum(-1).int().cpu()

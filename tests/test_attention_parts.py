@@ -218,3 +218,22 @@ def test_python_selection_refuses_sizes_by_their_own_status(lib, monkeypatch):
             with pytest.raises(binding.WanError) as e:
                 binding.op_block_select(x, x, 12, (3, 8, 8), (3, 8, 8), (1, 8, 8), kb, topk, workspace=workspace)
             assert e.value.name == "WAN_ESHAPE", (kb, topk)
+
+
+@pytest.mark.parametrize("masked", [False, True])
+def test_the_two_selections_of_the_oracle_agree(masked):
+    import math
+
+    import torch
+    from tests import attention_parts as R
+    g = torch.Generator().manual_seed(7)
+    for qg, kg, qb, kb, topk in (((3, 8, 8), (3, 8, 8), (1, 8, 8), (1, 4, 4), 5), ((2, 5, 9), (7, 9, 20), (4, 4, 8), (2, 4, 4), 11),
+                                 ((1, 1, 40), (1, 1, 16 * 90 - 3), (1, 1, 32), (1, 1, 16), 30)):
+        q = torch.randn((2, R.volume(qg), 256), generator=g).bfloat16()
+        k = torch.randn((2, R.volume(kg), 256), generator=g).bfloat16()
+        k[1, 16:48] = 0                                     # equal scores
+        k[1, 100, 3], k[1, 120, 130] = math.nan, math.inf
+        mask = torch.randint(0, 4, (R.block_count(qg, qb), R.block_count(kg, kb)), generator=g).to(torch.uint8) if masked else None
+        a = R.select(q, k, 2, qg, kg, qb, kb, topk, mask)
+        b = R.select_rows(q, k, 2, qg, kg, qb, kb, topk, mask)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
