@@ -173,3 +173,56 @@ def select_rows(q, k, heads, qg, kg, qb, kb, topk, mask=None):
     rank = rank.gather(-1, kind.gather(-1, rank).argsort(dim=-1, descending=True, stable=True))[..., :topk]
     keep = torch.where(kind.gather(-1, rank) > 0, rank, nk).sort(-1).values
     return torch.where(keep < nk, keep, -1).int().cpu(), (keep < nk).sum(-1).int().cpu()
+
+
+def check_rows(out, lse, ref, ref_lse, moved, size, keys):
+    """As check_attention, for a kernel that keeps p in fp32 (one and two new tokens): the output's rounding (2^-8),
+    the logits (130 roundings as there, and two more of the exponent's difference from the row's maximum), 2^-21 of
+    exp2 on both sides of the fraction, and the sums: at most keys / 8 additions of a lane one after the other, as
+    many rescalings, a few dozen where lanes, warps and parts meet, for numerator and denominator."""
+    logit = (132 * 2.0 ** -24) * size
+    sums = (keys / 2 + 256) * 2.0 ** -24 + 2.0 ** -20
+    bound = HALF_STEP * 1.01 * ref.abs() + (2 * logit[..., None] + sums) * moved + 1e-30
+    off = (out.to(DT) - ref).abs()
+    assert bool((off <= bound).all()), f"largest excess {(off - bound).max().item():.3g}"
+    if lse is not None:
+        none = ref_lse == -math.inf
+        assert torch.equal(lse.to(DT) == -math.inf, none)
+        off = torch.where(none, 0.0, (lse.to(DT) - ref_lse).abs())
+        far = off - (logit + sums + 2.0 ** -22 * ref_lse.abs().nan_to_num(0, 0, 0))
+        assert bool((far <= 0).all()), f"lse: largest excess {far.max().item():.3g}"
+
+
+# q . k / sqrt(128) in log2 units is -b for marked_query() and keys whose first two columns hold -b: bf16's 7.84375
+# and what is left of sqrt(128) / log2(e) (to 4e-7 of it), so p is a power of two and its rounding to bf16 exact.
+def marked_query(shape, device):
+    q = torch.zeros(shape, dtype=torch.bfloat16, device=device)
+    q[..., 0::HD] = 7.84375
+    q[..., 1::HD] = HD ** 0.5 * math.log(2.0) - 7.84375
+    return q
+
+
+def marked_keys(b, heads):
+    """Keys [n, heads * 128] of weights 2^-b."""
+    k = torch.zeros((*b.shape, heads, HD), dtype=torch.bfloat16, device=b.device)
+    k[..., :2] = -b[..., None, None].to(torch.bfloat16)
+    return k.flatten(-2)
+
+
+def marked_values(n, first, heads, device):
+    """Values [n, heads * 128]: of keys first .. first + 127 a one in a column of its own, else zero."""
+    v = torch.zeros((n, heads, HD), dtype=torch.bfloat16, device=device)
+    at = torch.arange(first, min(first + HD, n), device=device)
+    v[at, :, at - first] = 1
+    return v.flatten(-2)
+
+
+def check_marked(out, weight, first):
+    """out [..., heads, 128] where the keys have these weights [..., 1 or heads, n] of a row: each column is one key's.
+    The output's rounding, 4e-7 * b of the weights and the sums."""
+    total = weight.sum(-1, keepdim=True)
+    want = (weight / torch.where(total == 0, 1.0, total))[..., first:first + HD]
+    got = out[..., :want.shape[-1]].to(DT)
+    off = (got - want).abs()
+    assert bool((off <= want * (HALF_STEP * 1.01 + 2.0 ** -14)).all()), f"{(off / want.clamp(min=1e-30)).max().item():.3g}"
+    assert bool((out[..., want.shape[-1]:] == 0).all())
