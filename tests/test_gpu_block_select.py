@@ -183,3 +183,23 @@ def test_long_rows_rank_nan_and_infinite_scores(nk):
 def test_long_rows_at_the_ends_of_the_range(scale):
     q, k = rnd((1, 64, 128), 21, scale), rnd((1, 2100 * 16, 128), 22, scale)
     check(q, k, 1, (1, 1, 64), (1, 1, 2100 * 16), (1, 1, 16), (1, 1, 16), 99)
+
+
+# ------------------------------------------------------------------ rows of every length that a kernel is built for
+@pytest.mark.parametrize("nk", [n + d for n in (128, 256, 384, 512, 640, 768, 896, 1024, 1536, 2048) for d in (-31, 0, 1)])
+def test_rows_around_each_kernels_length(nk):
+    heads, topk = 2, nk // 6
+    args = (heads, (1, 1, 6 * 16), (1, 1, nk * 16), (1, 1, 16), (1, 1, 16))
+    q, k = rnd((1, 96, heads * 128), 31), rnd((1, nk * 16, heads * 128), 32)
+    k[0, 16:16 * (nk // 2), :128] = k[0, :16, :128].repeat(nk // 2 - 1, 1)      # head 0: half of the blocks are equal
+    k[0, 16 * (nk - 3):16 * (nk - 2)] *= 100
+    check(q, k, *args, topk)
+    mask = torch.randint(0, 5, (6, nk), generator=torch.Generator().manual_seed(33)).clamp(max=1).to(torch.uint8)
+    mask[1] = 0
+    mask[1, nk - 1] = 1
+    mask[2, -topk - 3:] = 2
+    mask[3, ::7] = 2
+    check(q, k, *args, topk, mask)
+    check(q, k, *args, nk, mask)
+    k[0, 16 * (nk - 1) + 3, 130] = math.nan                                     # head 1
+    check(q, k, *args, topk, mask)

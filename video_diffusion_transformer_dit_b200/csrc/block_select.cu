@@ -349,8 +349,11 @@ struct TopkParams {
     int *blocks, *counts;
 };
 // Up to 24 scores per lane seven CTAs share an SM, at 72 registers (eight, at 64, spill: 117
-// against 114 us for the pair's three kernels; six: 118).  NPL is the next of a few sizes:
-// the scans are unrolled over it, so their cost is NPL's, not the row's.
+// against 114 us for the pair's three kernels; six: 118).  The scans are unrolled over NPL, so
+// their cost is NPL's, not the row's: it is the next multiple of 4 up to 32 and of 16 beyond.
+// All three kernels of 336 x 800 blocks with NPL 28 against 32: 44 against 48 us; 336 x 1200
+// and 1500 with 48 against 64: 72 against 79 and 80 against 93; 336 x 200 with 8 against 12:
+// 25 against 26.
 template <int NPL>
 __global__ void __launch_bounds__(128, NPL <= 24 ? 7 : 1) block_topk_kernel(const __grid_constant__ TopkParams p) {
     using Bits = typename std::conditional<(NPL > 32), unsigned long long, uint32_t>::type;
@@ -796,8 +799,10 @@ __global__ void __launch_bounds__(256) block_topk64_kernel(const unsigned long l
 constexpr int SCORE64_SMEM = (128 * SCORE_Q + SCORE_K * K_PITCH) * 8;
 constexpr int TOPK64_SMEM = 225 * 1024;
 
-template <int NPL>
+template <int NPL = 4>
 void topk(const TopkParams& p, long long bh, cudaStream_t stream) {
+    if constexpr (NPL < MAX_FAST / 32)
+        if (p.nk > 32 * NPL) return topk<NPL + (NPL < 32 ? 4 : 16)>(p, bh, stream);
     block_topk_kernel<NPL><<<dim3((p.nq + 3) / 4, (unsigned)bh), 128, 0, stream>>>(p);
 }
 
@@ -865,13 +870,7 @@ cudaError_t launch_block_select(const void* q, long long ldq, const void* k, lon
         block_score_kernel<<<dim3((nk + ST - 1) / ST, (nq + ST - 1) / ST, (unsigned)bh), 128, 0, ctx.stream>>>(
             oq.unit, ok.unit, ok.norm, nq, nk, pitch, scores);
         const TopkParams p{scores, qm, km, oq.norm, ok.norm, mask, keys, nq, nk, pitch, topk_, blocks, counts};
-        const int per_lane = (nk + 31) / 32;
-        if (per_lane <= 4) topk<4>(p, bh, ctx.stream);
-        else if (per_lane <= 12) topk<12>(p, bh, ctx.stream);
-        else if (per_lane <= 20) topk<20>(p, bh, ctx.stream);
-        else if (per_lane <= 24) topk<24>(p, bh, ctx.stream);
-        else if (per_lane <= 32) topk<32>(p, bh, ctx.stream);
-        else topk<64>(p, bh, ctx.stream);
+        topk(p, bh, ctx.stream);
     } else {
         block_score64_kernel<<<dim3((nk + SCORE_K - 1) / SCORE_K, (nq + SCORE_Q - 1) / SCORE_Q, (unsigned)bh), 128,
                                SCORE64_SMEM, ctx.stream>>>(qm, km, mask, nq, nk, keys);
