@@ -4,7 +4,10 @@
  * These launch, one at a time, the same sm_100a kernels that wan_dit_forward()
  * strings together, so each step of the Wan DiT forward can be checked on its
  * own, and the attention operators over parts of the sequence (selected key
- * blocks, a paged cache), which the forward does not call.  Citations name the
+ * blocks, a paged cache).  wan_dit_forward() calls none of those; with its stages
+ * (wan_dit_sp_* of one rank) the caller puts the block-sparse attention in place
+ * of wan_dit_sp_attention(), while the cache is for callers that project q, k and
+ * v themselves (the stages rotate every sequence from frame 0).  Citations name the
  * page and section whose computation the kernel performs (see wandit.h for the
  * page list).  Conventions are those of
  * wandit.h: plain device pointers, `stream` is a cudaStream_t as void*, calls
@@ -137,7 +140,9 @@ typedef struct {
  * can depend on the order of additions) and keeps the topk best: equal scores go to
  * the lower block, a NaN ranks with -inf.  mask: uint8 [query blocks, key blocks] shared
  * by samples and heads, or NULL; 0 forbids a block, 1 leaves it to its score,
- * any other value takes it ahead of all scores.
+ * any other value takes it ahead of all scores.  A head with a NaN or an infinity
+ * among its keys is scored in 64 bits throughout: equal results, three to seven
+ * times the time where every head has one.
  *   blocks  int32 [B, heads, query blocks, topk]: the blocks kept, ascending,
  *           then -1 where fewer than topk are allowed
  *   counts  int32 [B, heads, query blocks]: how many are kept
@@ -162,7 +167,9 @@ WANDIT_API int64_t wan_op_block_select_workspace(int B, int heads, const wan_blo
  * and counts as wan_op_block_select writes them; the first counts[..] entries of
  * a list are read, a count is held to [0, topk]).  An entry that is no block of
  * the key grid is skipped; one listed twice counts twice.  A query whose list
- * holds nothing gets a zero row, and -inf in lse.
+ * holds nothing gets a zero row, and -inf in lse.  Scores, softmax and sums are
+ * f32; each probability is rounded to bf16 for its product with V, as in
+ * wan_op_attention, and the output once.
  *   lse   f32 [B, heads, query tokens], log of the softmax denominator with the
  *         row maximum in it (natural logarithm), or NULL
  *   workspace  as above, wan_op_attention_blocks_workspace() bytes; may be NULL
@@ -201,7 +208,7 @@ typedef struct {
  * position (s / (H W), s / W % H, s % W) when rope != 0 (frames have no limit;
  * split and pairs as wan_op_rmsnorm_rope), rounded once and stored; the value
  * row is copied.  With q != NULL the query rows get q_gain's norm and the same
- * rotation into q_out (may be q itself).  Rows t >= count[b], places past the
+ * rotation into q_out (may be q itself, with ldqo = ldq).  Rows t >= count[b], places past the
  * table (start[b] < 0 too) and pages that are not there are left as they were;
  * q_out is written for every t < count[b] with start[b] >= 0, and its other rows
  * are zeroed if zero_rest != 0 (for a buffer that is not q itself) or left.  Two
@@ -224,7 +231,9 @@ WANDIT_API wan_status wan_op_kv_append(const void* k, int64_t ldk, const void* v
  * other, as in a bidirectional forward, once they are appended.  Row (b, t) of q
  * / o at q + (b * T + t) * ldq.  lens[b] = 0 gives zero rows and -inf in lse
  * (f32 [B, heads, T], or NULL).  Memory of a page past the sequence's end is not
- * read into the result, whatever it holds.  Long caches are split and joined when
+ * read into the result, whatever it holds.  One and two new tokens keep their
+ * probabilities in f32, more round them to bf16 as wan_op_attention_blocks does:
+ * the same query's output differs in its last bits between the two.  Long caches are split and joined when
  * the query tiles are few: workspace as above,
  * wan_op_attention_paged_workspace() bytes.  Errors before any launch: WAN_EINVAL
  * for a null pointer, WAN_ESHAPE for B, T < 0, B * T > 2^30, B * heads > 2^20,

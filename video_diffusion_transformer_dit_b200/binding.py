@@ -629,7 +629,8 @@ def op_attention_blocks(q, k, v, heads, q_grid, k_grid, q_block, k_block, blocks
                         workspace=None, stream=None):
     """Attention of each query block over its listed key blocks (wan_op_attention_blocks): q, k, v bf16 [B, L, D],
     blocks int32 [B, heads, query blocks, topk], counts int32 [B, heads, query blocks]; lse f32 [B, heads, query
-    tokens] is filled if given.  Returns out, bf16 [B, query tokens, D]."""
+    tokens] is filled if given.  Probabilities are rounded to bf16 for their product with v.  Returns out, bf16
+    [B, query tokens, D]."""
     torch, dev = _torch(), q.device
     other = _elsewhere(dev, stream)
     if other is not None:
@@ -720,7 +721,8 @@ def op_attention_paged_workspace(B, heads, T, k_cache, v_cache, table) -> int:
 def op_attention_paged(q, k_cache, v_cache, table, lens, heads, out=None, lse=None, workspace=None, stream=None):
     """Attention of T new tokens per sequence over its cached places [0, lens[b]) (wan_op_attention_paged): q bf16
     [B, T, D], caches bf16 [pages, page size, D], table int32 [B, pages], lens int32 [B]; lse f32 [B, heads, T] is
-    filled if given.  Returns out, bf16 [B, T, D]."""
+    filled if given.  From three tokens on probabilities are rounded to bf16 for their product with v.  Returns
+    out, bf16 [B, T, D]."""
     torch, dev = _torch(), q.device
     other = _elsewhere(dev, stream)
     if other is not None:

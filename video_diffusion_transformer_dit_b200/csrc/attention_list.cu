@@ -16,9 +16,11 @@
 // 256 columns of tensor memory: O_t (128) and two S buffers of 64 columns, each
 // overwritten by its P (bf16, 32 columns).  In step k of its unit a stream issues
 // S(k) = Q K_k^T into the one buffer and O += P(k-1) V_(k-1) from the other, so
-// the softmax finds S(k) finished when it is done with tile k - 1 (with one
-// 128-key S per stream the softmax and the MMAs of a stream take turns: 2.0 ms at
-// the 480p size below).  The streams share nothing but the SM: each has its producer,
+// the softmax finds S(k) finished when it is done with tile k - 1.  (The first
+// version had one 128-key S per stream, softmax and MMAs of a stream in turns, and
+// one producer and one issuer for both streams: 2.0 ms at the 480p size below.
+// 128-key tiles with a producer and an issuer per stream have not been measured.)
+// The streams share nothing but the SM: each has its producer,
 // its issuer, its softmax warps and its ring of five 16 KB slots for K and V tiles
 // in the order K(k), V(k - 1).  Stream t walks units blockIdx.x * 2 + t,
 // + 2 * gridDim.x, ...
@@ -43,7 +45,7 @@
 // normalised fp32 rows and their log-sum-exp, and list_join_kernel joins them.
 //
 // Measured (12 heads, 32760 tokens of a 480p clip; Tflop/s of the tiles computed):
-//   blocks, 336 query blocks of 128 x 78 of 624 key blocks of 64: 1.13-1.2 ms cold, 1.30
+//   blocks, 336 query blocks of 128 x 78 of 624 key blocks of 64: 1.13-1.2 ms cold, 1.29-1.31
 //     in a long run, where the power limit holds the clock at 1.7 GHz; 1.03-1.15 Pflop/s,
 //     tensor pipe 57 %.  A third of the rows and keys are padding of blocks at the grid's
 //     edges.  What bounds it: S = Q K^T with 64 keys reads both operands from shared
@@ -774,6 +776,9 @@ __global__ void __launch_bounds__(alist::THREADS, 1)
 // lane, 116 and 128 registers), in two CTAs, or in four where there are more lists than
 // such units: each list ends with the meeting of its warps (256 sequences of 64 tokens: 34.5
 // against 44.1 us, of 130: 52 against 64; one of 4096: 11.9 against 10.1, more parts to join).
+// The rule goes by the number of lists alone, as lengths are known on the device only: with
+// long lists the two are within 2 %, 300 to 1280 of 2000 to 16380 places 62 to 352 us in two CTAs
+// and 63 to 355 in four (two tokens: 66 to 365 and 67 to 365).
 template <int R, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) paged_rows_kernel(const __nv_bfloat16* __restrict__ q, long long ldq,
                                                             const __nv_bfloat16* __restrict__ k,
@@ -1050,8 +1055,11 @@ namespace {
 // Splits of each list: the number that takes the least time in tile steps, over the
 // waves of two units per SM.  A unit costs its tiles plus five steps of filling and
 // draining, a split one another for its fp32 rows, and the join reads them all again.
-// In ten shapes (1 to 1560 rows, 30 to 2049 tiles, every number of splits up to 49) its
-// choice was within 3 % of the best one, and 5 % in one; a wave more costs 30 to 50 %.
+// With the tiles, in ten shapes (1 to 1560 rows, 30 to 2049 tiles, every number of splits
+// up to 49), its choice was within 3 % of the best one, and 5 % in one; a wave more costs 30
+// to 50 %.  paged_rows_kernel is planned by the same numbers: in nine shapes of 5 to 40 heads,
+// 700 to 131040 places, within 5 % of the best of fourteen tried.  One head alone over 131040
+// places is not: 42.8 us with 296 parts, which one warp per row joins, 27.6 with 111.
 int list_splits(long long per, long long max_tiles, int rows, int streams = 2 * alist::PLAN_SMS) {
     if (per <= 0 || per >= 8 * streams) return 1;
     int best = 1;

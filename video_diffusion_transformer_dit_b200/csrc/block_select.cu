@@ -12,20 +12,26 @@
 //                       length in fp16, and their norms;
 //   block_score_kernel  unit products on the tensor cores times the key's norm:
 //                       within SCORE_ERROR |k| of the 64-bit score over |q|;
-//   block_topk_kernel   the topk-th best of a row by bisection; only blocks that
-//                       the error lets lie on either side of the border (seven or
-//                       so of several hundred) are scored again, in fp64, and
-//                       ranked by that.
+//   block_topk_kernel   the topk-th best of a row, from a first place by the row's mean
+//                       and spread through interpolation (bisection where that does
+//                       not settle it); only blocks that the error lets lie on either
+//                       side of the border (seven or so of several hundred) are scored
+//                       again, in fp64, and ranked by that.
 // (With hi + lo parts and three products fewer are scored again, but the products
 // and their operands cost more than that saves: 30 against 14 us of the pair's.)
 // Longer rows: block_score64_kernel and block_topk64_kernel, all in fp64.
 //
 // Measured, us: means 75 (5.4 TB/s), scores 14, top-k 28 of the 480p pair (B = 2, 12
 // heads, 32760 tokens, 336 x 624 blocks); 248 (6.3 TB/s), 44 and 93 with 40 heads, 75600
-// tokens, 720 x 720 blocks and a mask.  The means are bound by memory; the scores by
+// tokens, 720 x 720 blocks and a mask.  The larger case's means run at the rate of a copy;
+// the pair's are held by the conversions to fp64 (74 % of their pipe) as much as by memory
+// (66 % of DRAM's peak), in many short CTAs; the scores are bound by
 // their way through the L2, and 64 x 128 tiles, which read a quarter less, take 2 us off
 // the 44; the top-k by instruction issue (65 %): 2300 per row of 720.  Starting each kernel
 // while the one before it drains costs the large cases more (1 %) than it saves.
+// A NaN or an infinity in a head's keys leaves no bound for its rows: all their scores are
+// taken in fp64 by block_topk_kernel, a warp per row.  With one in every head 355 us for 122
+// (pair), 2590 for 394 (40 heads).
 #include <cuda_fp16.h>
 
 #include <cfloat>
