@@ -7,10 +7,9 @@
  * blocks, a paged cache).  wan_dit_forward() calls none of those; with its stages
  * (wan_dit_sp_* of one rank) the caller puts the block-sparse attention in place
  * of wan_dit_sp_attention(), while the cache is for callers that project q, k and
- * v themselves (the stages rotate every sequence from frame 0).  Citations name the
- * page and section whose computation the kernel performs (see wandit.h for the
- * page list).  Conventions are those of
- * wandit.h: plain device pointers, `stream` is a cudaStream_t as void*, calls
+ * v themselves (the stages rotate every sequence from frame 0).  Citations name
+ * the page and section whose computation the kernel performs (see wandit.h for
+ * the page list).  Conventions are those of wandit.h: plain device pointers, `stream` is a cudaStream_t as void*, calls
  * are asynchronous, nothing is retained after the call, shape errors are
  * reported before any launch, and wan_op_sync() reports a kernel wait that ran
  * out of time.  All matrices are dense row-major with the given leading
@@ -208,8 +207,8 @@ typedef struct {
  * position (s / (H W), s / W % H, s % W) when rope != 0 (frames have no limit;
  * split and pairs as wan_op_rmsnorm_rope), rounded once and stored; the value
  * row is copied.  With q != NULL the query rows get q_gain's norm and the same
- * rotation into q_out (may be q itself, with ldqo = ldq).  Rows t >= count[b], places past the
- * table (start[b] < 0 too) and pages that are not there are left as they were;
+ * rotation into q_out (may be q itself, with ldqo = ldq).  Rows t >= count[b],
+ * places past the table (start[b] < 0 too) and pages that are not there are left as they were;
  * q_out is written for every t < count[b] with start[b] >= 0, and its other rows
  * are zeroed if zero_rest != 0 (for a buffer that is not q itself) or left.  Two
  * sequences that share a page must not write the same place.
@@ -233,8 +232,8 @@ WANDIT_API wan_status wan_op_kv_append(const void* k, int64_t ldk, const void* v
  * (f32 [B, heads, T], or NULL).  Memory of a page past the sequence's end is not
  * read into the result, whatever it holds.  One and two new tokens keep their
  * probabilities in f32, more round them to bf16 as wan_op_attention_blocks does:
- * the same query's output differs in its last bits between the two.  Long caches are split and joined when
- * the query tiles are few: workspace as above,
+ * the same query's output differs in its last bits between the two.  Long caches
+ * are split and joined when the query tiles are few: workspace as above,
  * wan_op_attention_paged_workspace() bytes.  Errors before any launch: WAN_EINVAL
  * for a null pointer, WAN_ESHAPE for B, T < 0, B * T > 2^30, B * heads > 2^20,
  * strides, pointers or a cache outside the limits above, or a workspace that is
