@@ -9,11 +9,12 @@
  * of wan_dit_sp_attention(), while the cache is for callers that project q, k and
  * v themselves (the stages rotate every sequence from frame 0).  Citations name
  * the page and section whose computation the kernel performs (see wandit.h for
- * the page list).  Conventions are those of wandit.h: plain device pointers, `stream` is a cudaStream_t as void*, calls
- * are asynchronous, nothing is retained after the call, shape errors are
- * reported before any launch, and wan_op_sync() reports a kernel wait that ran
- * out of time.  All matrices are dense row-major with the given leading
- * dimension (in elements); bf16 means IEEE bfloat16, f32 means float.
+ * the page list).  Conventions are those of wandit.h: plain device pointers,
+ * `stream` is a cudaStream_t as void*, calls are asynchronous, nothing is
+ * retained after the call, shape errors are reported before any launch, and
+ * wan_op_sync() reports a kernel wait that ran out of time.  All matrices are
+ * dense row-major with the given leading dimension (in elements); bf16 means IEEE
+ * bfloat16, f32 means float.
  */
 #ifndef WANDIT_OPS_H
 #define WANDIT_OPS_H
